@@ -73,15 +73,6 @@ __device__ __forceinline__ void load8(const CtaArgs& g, int64_t m, int k, float 
   }
 }
 
-// two fp32 values -> their bf16 bits (low half the first), round to nearest,
-// ties to even, one V_CVT_PK_BF16_F32 (a NaN stays a NaN)
-__device__ __forceinline__ uint32_t bf16x2_rne(float lo, float hi) {
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  const f32x2_t v = {lo, hi};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-}
-
 __device__ __forceinline__ void store8(const CtaArgs& g, int64_t m, int k, const float (&v)[8]) {
   if (g.bf16) {
     uint32_t w[4];

@@ -27,10 +27,6 @@ int32_t hip_status(hipError_t e) { return e == hipSuccess ? LOOPQ_OK : LOOPQ_ERR
 // events recorded on its own stream; loopq_timing_read sums their elapsed
 // times per kernel id.  Events are pooled and reused after a read or reset.
 // ---------------------------------------------------------------------------
-struct TimingRec {
-  int kid;
-  hipEvent_t start, stop;
-};
 std::mutex g_timing_mu;
 bool g_timing_on = false;
 std::vector<TimingRec> g_timing_recs;
@@ -50,27 +46,6 @@ hipEvent_t pooled_event() {
 // Set while loopq_w4a4_linear_noalloc runs on this thread: its launches take
 // no timing records (a record may create HIP events, which allocate).
 thread_local bool t_no_alloc = false;
-
-struct TimingScope {
-  bool on = false;
-  TimingRec rec{};
-  hipStream_t s;
-  TimingScope(int kid, hipStream_t stream) : s(stream) {
-    if (t_no_alloc) return;
-    std::lock_guard<std::mutex> lk(g_timing_mu);
-    if (!g_timing_on) return;
-    rec.kid = kid;
-    rec.start = pooled_event();
-    rec.stop = pooled_event();
-    if (!rec.start || !rec.stop) return;
-    on = hipEventRecord(rec.start, s) == hipSuccess;
-  }
-  ~TimingScope() {
-    if (!on) return;
-    std::lock_guard<std::mutex> lk(g_timing_mu);
-    if (hipEventRecord(rec.stop, s) == hipSuccess) g_timing_recs.push_back(rec);
-  }
-};
 
 void recycle_locked() {
   for (auto& r : g_timing_recs) {
@@ -1308,6 +1283,23 @@ int32_t loopq_timing_read(int32_t n, double* ms_host, int64_t* launches_host) {
 }  // extern "C"
 
 namespace loopq {
+
+TimingScope::TimingScope(int kid, hipStream_t stream) : s(stream) {
+  if (t_no_alloc) return;
+  std::lock_guard<std::mutex> lk(g_timing_mu);
+  if (!g_timing_on) return;
+  rec.kid = kid;
+  rec.start = pooled_event();
+  rec.stop = pooled_event();
+  if (!rec.start || !rec.stop) return;
+  on = hipEventRecord(rec.start, s) == hipSuccess;
+}
+
+TimingScope::~TimingScope() {
+  if (!on) return;
+  std::lock_guard<std::mutex> lk(g_timing_mu);
+  if (hipEventRecord(rec.stop, s) == hipSuccess) g_timing_recs.push_back(rec);
+}
 
 int device_cu_count() {
   int dev = 0;

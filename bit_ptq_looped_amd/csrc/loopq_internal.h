@@ -250,6 +250,20 @@ hipError_t launch_cta(const void* h, int bf16, int64_t rows, int K, const float*
                       void* out, hipStream_t s);
 int cta_max_rank();
 
+// Timing hooks (loopq_api.hip): while they are on, the scope's launches on
+// `stream` are bracketed by two HIP events under kernel id `kid`.
+struct TimingRec {
+  int kid;
+  hipEvent_t start, stop;
+};
+struct TimingScope {
+  bool on = false;
+  TimingRec rec{};
+  hipStream_t s;
+  TimingScope(int kid, hipStream_t stream);
+  ~TimingScope();
+};
+
 hipError_t reset_status(hipStream_t s);
 hipError_t read_status(int* host_status, hipStream_t s);
 

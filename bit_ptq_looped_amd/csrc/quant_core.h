@@ -20,6 +20,15 @@ __device__ __forceinline__ float bf16_bits_to_float(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
 }
 
+// two fp32 values -> their bf16 bits (low half the first), round to nearest,
+// ties to even, one V_CVT_PK_BF16_F32 (a NaN stays a NaN)
+__device__ __forceinline__ uint32_t bf16x2_rne(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
 // max over the 8 consecutive lanes of a group: quad swaps 1 and 2, then the
 // half-row mirror pairs each lane with one of the other quad (DPP, no LDS)
 __device__ __forceinline__ float group8_max(float v) {

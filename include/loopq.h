@@ -447,7 +447,9 @@ typedef enum {
   LOOPQ_KERNEL_DECODE = 3,          /* few-row linear: transform, quantizer and product in one launch */
   LOOPQ_KERNEL_HESSIAN = 4,         /* trajectory Hessian accumulation (one record per call) */
   LOOPQ_KERNEL_QUANT_TOKEN = 5,     /* per-token quantizer */
-  LOOPQ_KERNEL_CTA = 6              /* CTA loop-transition adapter */
+  LOOPQ_KERNEL_CTA = 6,             /* CTA loop-transition adapter */
+  LOOPQ_KERNEL_ATTN = 7,            /* attention over the paged cache (loopq_kv.h; one record per call) */
+  LOOPQ_KERNEL_KV = 8               /* cache pages: reserve, write, fork, trim, compact, copy (one record per call) */
 } loopq_kernel_id;
 
 /* Turn the hooks on (1) or off (0).  Host only; cheap. */
