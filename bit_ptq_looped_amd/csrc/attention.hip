@@ -42,20 +42,25 @@ constexpr int kDecodeGroups = 512;   // work-groups of the decode launch, four p
 constexpr int kDecodePieces = kDecodeGroups * 4;
 constexpr int kDecodeRows = 16;      // query heads of an item
 constexpr int kDecodeKeys = 32;      // keys of a tile
-constexpr int kPrefillPieces = 512;  // work-groups of the prefill launch
+constexpr int kPrefillGroups = 512;  // work-groups of the prefill launch
+constexpr int kPrefillSlots = 2 * kPrefillGroups;
 constexpr int kPrefillRows = 128;    // (query, head) rows of an item
 constexpr int kPrefillKeys = 64;
 
 // what a launch needs beside the caller's arguments
 struct AttnPlan {
-  float* part;        // partial results: [piece][2][rows][head_dim], then m and l
-  float* ml;          // [piece][2][2][rows]
-  const uint16_t* zeros;  // 16 zero bytes, cleared by the plan launch
-  int64_t* row_unit;  // prefill: tiles before each row, [rows + 1]
-  int64_t* row_tiles; // prefill: query tiles before each row, [rows + 1]
-  int64_t* tile_unit; // prefill: key tiles before each query tile, within its row and key head
-  float c;            // |scale| log2(e), or 1 for a scale of 0
-  float qmul;         // sign of the scale: queries are taken times this
+  float* part;            // partial results: [slot][rows][head_dim], then
+  float* ml;              // their m and l: [slot][2][rows]
+  int64_t* row_task;      // prefill: tasks before each row, [rows + 1]
+  int64_t* row_slot;      // prefill: slots before each row, [rows + 1]
+  int64_t* row_tiles;     // prefill: query tiles before each row, [rows + 1]
+  int32_t* tile_task;     // prefill: tasks before each query tile, within its row and key head
+  int32_t* tile_slot;     // the same for slots
+  int64_t* head;          // prefill: {most key tiles of a task}, then
+  int32_t* next;          // tasks handed out, of each eighth of the tasks
+  const uint16_t* zeros;  // 256 zero bytes, cleared by the plan launch
+  float c;                // |scale| log2(e), or 1 for a scale of 0
+  float qmul;             // sign of the scale: queries are taken times this
 };
 
 __device__ __forceinline__ int row_len(const AttnArgs& a, int row) {
@@ -137,7 +142,8 @@ __device__ __forceinline__ void block_prefix(int n, int64_t* out, F f) {
 }
 
 // the last i in [0, n) with p[i] <= u
-__device__ __forceinline__ int find(const int64_t* p, int n, int64_t u) {
+template <class T>
+__device__ __forceinline__ int find(const T* p, int n, T u) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -207,12 +213,12 @@ struct Planes {
 
 // Place of 16-byte chunk ch of a key's row in a tile of 2^LOG keys in LDS:
 // blocks of four chunks (32 columns), the key's 64 bytes of each block in one
-// run.  Keys are permuted by the block and chunks by the key, so that writes of
-// whole rows, reads of one chunk of 16 keys and transposing reads of four keys
-// each spread over all banks.
-template <int LOG>
+// run, chunks permuted by the key: reads of one chunk of 16 keys and transposing
+// reads of four keys each spread over all banks.  ROWS also permutes the keys by
+// the block, which does the same for writes of whole rows.
+template <int LOG, bool ROWS>
 __device__ __forceinline__ int chunk_at(int key, int ch) {
-  return ((ch >> 2) << (LOG + 2)) + ((key ^ ((ch >> 2) & 3)) << 2) + ((ch & 3) ^ ((key >> 2) & 3));
+  return ((ch >> 2) << (LOG + 2)) + ((ROWS ? key ^ ((ch >> 2) & 3) : key) << 2) + ((ch & 3) ^ ((key >> 2) & 3));
 }
 
 __device__ __forceinline__ u32x2 read_tr(const u32x4* tile, int chunk, int half) {
@@ -284,10 +290,10 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
       int page = -1;
       if (sees(a, pos, j)) {
         page = table[j >> a.page_shift];
-        if (page >= a.num_pages) page = -1;
       }
-      return page;
+      return page;  // as it stands in the table: the load is not waited for here
     };
+    const auto real = [&](int page) { return (uint32_t)page < (uint32_t)a.num_pages ? page : -1; };
     u32x4 kr[2][D / 32], vr[NV];
     const auto load_tile = [&](int i, int page) {
       const int j0 = tl.at(i) << 5;
@@ -310,7 +316,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
       }
     };
 
-    int page = page_of(first);
+    int page = real(page_of(first));
     uint32_t seen = (uint32_t)__ballot(page >= 0);
     load_tile(first, page);
     page = first + 1 < last ? page_of(first + 1) : -1;
@@ -330,12 +336,13 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
 #pragma unroll
       for (int x = 0; x < NV; ++x) {
         const int at = lane + 64 * x, key = at / C, ch = at - key * C;
-        tile[chunk_at<5>(key, ch)] = vr[x];
+        tile[chunk_at<5, true>(key, ch)] = vr[x];
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       const uint32_t now = seen;
       if (i + 1 < last) {
+        page = real(page);
         seen = (uint32_t)__ballot(page >= 0);
         load_tile(i + 1, page);
         page = i + 2 < last ? page_of(i + 2) : -1;
@@ -354,7 +361,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
       top *= pl.c;
       if (__any(top > m)) {
         const float mn = fmaxf(m, top);
-        const float f = exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
         m = mn;
         l *= f;
 #pragma unroll
@@ -372,7 +379,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         const int x = lane & 15, key = 4 * g + (x >> 2), ch = 2 * d + ((x & 3) >> 1);
-        const bf16x8 vt = join_halves(read_tr(tile, chunk_at<5>(key, ch), x & 1), read_tr(tile, chunk_at<5>(key + 16, ch), x & 1));
+        const bf16x8 vt = join_halves(read_tr(tile, chunk_at<5, true>(key, ch), x & 1), read_tr(tile, chunk_at<5, true>(key + 16, ch), x & 1));
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, w[n], o[d], 0, 0, 0);
       }
@@ -416,22 +423,21 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
         }
 }
 
-// Joins the pieces w0 .. w1 of one item for one of its rows, one wave: columns
-// lane and lane + 64 of the result (unscaled by 1 / l) and l.
-template <int D, int ROWS>
-__device__ __forceinline__ float join_row(const AttnPlan& pl, int64_t w0, int64_t w1, int slot0, int r, float (&o)[2]) {
+// Joins the n parts of one item for one of its rows, one wave: columns lane and
+// lane + 64 of the result (unscaled by 1 / l) and l.
+template <int D, int ROWS, class F>
+__device__ __forceinline__ float join_row(const AttnPlan& pl, int n, int r, F slot_of, float (&o)[2]) {
   const int lane = threadIdx.x & 63;
   float m = -INFINITY;
-  for (int64_t w = w0 + lane; w <= w1; w += 64)
-    m = fmaxf(m, pl.ml[(w * 2 + (w == w0 ? slot0 : 0)) * 2 * ROWS + r]);
+  for (int i = lane; i < n; i += 64) m = fmaxf(m, pl.ml[slot_of(i) * 2 * ROWS + r]);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   const float ref = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
   o[0] = o[1] = 0.0f;
 #pragma unroll 4
-  for (int64_t w = w0; w <= w1; ++w) {
-    const int64_t slot = w * 2 + (w == w0 ? slot0 : 0);
+  for (int i = 0; i < n; ++i) {
+    const int64_t slot = slot_of(i);
     const float f = __builtin_amdgcn_exp2f(pl.ml[slot * 2 * ROWS + r] - ref);
     const float* p = pl.part + (slot * ROWS + r) * D;
     l = fmaf(f, pl.ml[(slot * 2 + 1) * ROWS + r], l);
@@ -472,7 +478,8 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a, AttnPlan p
   const int kvh = item / gts, gt = item - kvh * gts;
   for (int r = threadIdx.x >> 6; r < min(kDecodeRows, a.group - gt * kDecodeRows); r += 4) {
     float o[2];
-    const float l = join_row<D, kDecodeRows>(pl, w0, w1, i0 != w0 * piece, r, o);
+    const int64_t slot0 = w0 * 2 + (i0 != w0 * piece);
+    const float l = join_row<D, kDecodeRows>(pl, (int)(w1 - w0) + 1, r, [&](int i) { return i ? (w0 + i) * 2 : slot0; }, o);
     store_row<D>(a, row * a.ldo + (int64_t)(kvh * a.group + gt * kDecodeRows + r) * D, o, l);
   }
 }
@@ -490,124 +497,174 @@ __device__ __forceinline__ Tiles tile_keys(const AttnArgs& a, int t, int n, int 
   return visible_tiles(a, *lo, *hi, 6);
 }
 
-// One work-group: where every row's and every query tile's key tiles start.
-__global__ __launch_bounds__(1024) void prefill_plan_kernel(AttnArgs a, AttnPlan pl) {
-  __shared__ int64_t part[16], part2[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (tid < 4) reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(pl.zeros))[tid] = 0;
-  int64_t base = 0, base2 = 0;
-  // rows one after another if they are long, a thread each for their sums
-  for (int r0 = 0; r0 < a.rows; r0 += 1024) {
-    const int r = r0 + tid;
-    int64_t units = 0, tiles = 0;
-    if (r < a.rows) {
-      int first;
-      const int n = row_queries(a, r, &first);
-      tiles = query_tiles(a, n);
-    }
-    int64_t x = tiles;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int64_t y = __shfl_up(x, off, 64);
-      if (lane >= off) x += y;
-    }
-    if (lane == 63) part[wave] = x;
-    __syncthreads();
-    int64_t before = base, all = base;
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? part[w] : 0;
-      all += part[w];
-    }
-    if (r < a.rows) pl.row_tiles[r] = before + x - tiles;
-    base = all;
-    (void)units;
-    __syncthreads();
-  }
-  if (tid == 0) pl.row_tiles[a.rows] = base;
-  __syncthreads();
-  // key tiles before each query tile of its row: a wave per row
-  for (int r = wave; r < a.rows; r += 16) {
-    int first;
-    const int n = row_queries(a, r, &first), len = row_len(a, r), qt = query_tiles(a, n);
-    int64_t sum = 0;
-    for (int t0 = 0; t0 < qt; t0 += 64) {
-      const int t = t0 + lane;
-      int lo, hi;
-      const int64_t v = t < qt ? tile_keys(a, t, n, len, &lo, &hi).n : 0;
-      int64_t x = v;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int64_t y = __shfl_up(x, off, 64);
-        if (lane >= off) x += y;
-      }
-      if (t < qt) pl.tile_unit[pl.row_tiles[r] + t] = sum + x - v;
-      sum += __shfl(x, 63, 64);
-    }
-    if (lane == 0) pl.row_unit[r] = sum * a.heads;
-  }
-  __syncthreads();
-  for (int r0 = 0; r0 < a.rows; r0 += 1024) {
-    const int r = r0 + tid;
-    const int64_t v = r < a.rows ? pl.row_unit[r] : 0;
-    int64_t x = v;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int64_t y = __shfl_up(x, off, 64);
-      if (lane >= off) x += y;
-    }
-    if (lane == 63) part2[wave] = x;
-    __syncthreads();
-    int64_t before = base2, all = base2;
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? part2[w] : 0;
-      all += part2[w];
-    }
-    if (r < a.rows) pl.row_unit[r] = before + x - v;
-    base2 = all;
-    __syncthreads();
-  }
-  if (tid == 0) pl.row_unit[a.rows] = base2;
+// the larger of lanes x and x + 32, in both
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-__device__ __forceinline__ int64_t prefill_piece(int64_t total) {
-  const int64_t n = (total + kPrefillPieces - 1) / kPrefillPieces;
-  return n < 4 ? 4 : n;
+// x of the wave's first lane, as a scalar
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// inclusive sum over the wave
+__device__ __forceinline__ int64_t wave_sum(int64_t x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  return x;
+}
+
+// p[0 .. n) to its exclusive prefix, p[n] the sum, by 1024 threads; barriers on both sides
+__device__ __forceinline__ int64_t prefix_in_place(int64_t* p, int n) {
+  __shared__ int64_t part[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t base = 0;
+  __syncthreads();
+  for (int i0 = 0; i0 < n; i0 += 1024) {
+    const int i = i0 + tid;
+    const int64_t v = i < n ? p[i] : 0, x = wave_sum(v);
+    if (lane == 63) part[wave] = x;
+    __syncthreads();
+    int64_t before = base;
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? part[w] : 0;
+      base += part[w];
+    }
+    if (i < n) p[i] = before + x - v;
+    __syncthreads();
+  }
+  if (tid == 0) p[n] = base;
+  __syncthreads();
+  return base;
+}
+
+// One work-group.  A task is an item or, where an item has more than L key
+// tiles, a part of it of at most L; L is a work-group's even share of all key
+// tiles, so that few long items are split over the whole chip and many stay
+// whole.  Slots take the results of split items' tasks: at most 2 tiles / L.
+__global__ __launch_bounds__(1024) void prefill_plan_kernel(AttnArgs a, AttnPlan pl) {
+  __shared__ unsigned long long s_sum;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (tid < 64) reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(pl.zeros))[tid] = 0;
+  if (tid < 8) pl.next[tid] = 0;
+  if (tid == 0) s_sum = 0;
+  for (int r = tid; r < a.rows; r += 1024) {
+    int first;
+    pl.row_tiles[r] = query_tiles(a, row_queries(a, r, &first));
+  }
+  prefix_in_place(pl.row_tiles, a.rows);
+  for (int pass = 0; pass < 2; ++pass) {
+    const int64_t L = pass ? pl.head[0] : 0;
+    for (int r = wave; r < a.rows; r += 16) {  // a wave per row
+      int first;
+      const int n = row_queries(a, r, &first), len = row_len(a, r), qt = query_tiles(a, n);
+      int64_t tasks = 0, slots = 0;
+      for (int t0 = 0; t0 < qt; t0 += 64) {
+        const int t = t0 + lane;
+        int lo, hi;
+        const int64_t keys = t < qt ? tile_keys(a, t, n, len, &lo, &hi).n : 0;
+        if (pass == 0) {
+          tasks += keys;
+        } else {
+          const int64_t parts = (keys + L - 1) / L, x = wave_sum(parts), y = wave_sum(parts > 1 ? parts : 0);
+          if (t < qt) {
+            pl.tile_task[pl.row_tiles[r] + t] = (int32_t)(tasks + x - parts);
+            pl.tile_slot[pl.row_tiles[r] + t] = (int32_t)(slots + y - (parts > 1 ? parts : 0));
+          }
+          tasks += __shfl(x, 63, 64);
+          slots += __shfl(y, 63, 64);
+        }
+      }
+      if (pass == 0) {
+        const int64_t x = wave_sum(tasks);
+        if (lane == 63) atomicAdd(&s_sum, (unsigned long long)(x * a.heads));
+      } else if (lane == 0) {
+        pl.row_task[r] = tasks * a.heads;
+        pl.row_slot[r] = slots * a.heads;
+      }
+    }
+    __syncthreads();
+    if (pass == 0 && tid == 0) pl.head[0] = max((int64_t)4, ((int64_t)s_sum + kPrefillGroups - 1) / kPrefillGroups);
+    __syncthreads();
+  }
+  prefix_in_place(pl.row_task, a.rows);
+  prefix_in_place(pl.row_slot, a.rows);
 }
 
 struct PrefillItem {
-  int row, kvh, tile, n, len, first;  // first: the row's first query
-  int lo, hi;                         // positions of the tile's queries
+  int row, kvh, tile, part, n, len, first;  // first: the row's first query
+  int lo, hi;                               // positions of the tile's queries
   Tiles tl;
-  int64_t i0;                         // its first unit
+  int from, to;                             // key tiles of the task
+  int64_t slot;                             // of the item's first task, if there are several
 };
-__device__ __forceinline__ PrefillItem prefill_item(const AttnArgs& a, const AttnPlan& pl, int64_t u) {
+// Task x by the prefixes of tasks, or of slots.  Within a key head the query
+// tiles go from the last to the first, which has the fewest keys.
+__device__ __forceinline__ PrefillItem prefill_item(const AttnArgs& a, const AttnPlan& pl, int64_t x, bool by_slot) {
   PrefillItem it;
-  it.row = find(pl.row_unit, a.rows, u);
+  const int64_t* rows = by_slot ? pl.row_slot : pl.row_task;
+  it.row = find(rows, a.rows, x);
   it.n = row_queries(a, it.row, &it.first);
   it.len = row_len(a, it.row);
-  const int64_t base = pl.row_unit[it.row], per = (pl.row_unit[it.row + 1] - base) / a.heads;
-  it.kvh = (int)((u - base) / per);
-  const int64_t in_head = u - base - it.kvh * per;
-  const int64_t* tu = pl.tile_unit + pl.row_tiles[it.row];
-  it.tile = find(tu, (int)(pl.row_tiles[it.row + 1] - pl.row_tiles[it.row]), in_head);
+  const int64_t per = (rows[it.row + 1] - rows[it.row]) / a.heads;
+  x -= rows[it.row];
+  it.kvh = (int)(x / per);
+  x -= it.kvh * per;
+  if (!by_slot) x = per - 1 - x;
+  const int64_t t0 = pl.row_tiles[it.row];
+  const int32_t* before = (by_slot ? pl.tile_slot : pl.tile_task) + t0;
+  it.tile = find(before, (int)(pl.row_tiles[it.row + 1] - t0), (int32_t)x);
+  it.part = (int)x - before[it.tile];
   it.tl = tile_keys(a, it.tile, it.n, it.len, &it.lo, &it.hi);
-  it.i0 = base + it.kvh * per + tu[it.tile];
+  const int64_t L = pl.head[0];
+  it.from = (int)(it.part * L);
+  it.to = (int)min((it.part + 1) * L, (int64_t)it.tl.n);
+  it.slot = pl.row_slot[it.row] + it.kvh * ((pl.row_slot[it.row + 1] - pl.row_slot[it.row]) / a.heads) + pl.tile_slot[t0 + it.tile];
   return it;
 }
 
-// 16 bytes per lane from global memory to LDS, lane x's at dst + 16 x, without
-// passing the registers.  The compiler does not see the write: a reader waits
-// for loads_done() and the barrier after it.
-__device__ __forceinline__ void load_lds16(const void* src, const void* dst) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)dst;
-  // one wait state between the write of m0 and the load that reads it
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(at)), "v"(src)
+// The next task for a work-group of eighth e, or -1: each XCD has an eighth of
+// the tasks (neighbours share keys, and with them an L2), then helps out in the
+// others.  Which work-group takes a task does not change its result.
+__device__ __forceinline__ int64_t next_task(const AttnPlan& pl, int64_t tasks, int* e, int* tries) {
+  for (; *tries < 8; ++*tries, *e = (*e + 1) & 7) {
+    const int64_t lo = tasks * *e / 8, hi = tasks * (*e + 1) / 8;
+    const int64_t x = lo + atomicAdd(pl.next + *e, 1);
+    if (x < hi) return x;
+  }
+  return -1;
+}
+
+// 16 bytes per lane from src + OFF (bytes, per lane) to LDS at byte dst + 16
+// lane (dst a scalar), without passing the registers.  The compiler does not see the write: a
+// reader waits for loads_done() and the barrier after it.  The offset counts for
+// the target, too; one wait state lies between the write of m0 and its use.
+template <int OFF>
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(dst - OFF), "v"(src), "n"(OFF)
                : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
+}
+
+// whether every key of a tile of 64 has a page
+__device__ __forceinline__ bool tile_has_pages(const AttnArgs& a, const int32_t* table, int tile) {
+  bool ok = true;
+  for (int j = tile << 6; j < (tile + 1) << 6; j += min(64, 1 << a.page_shift))
+    ok &= (uint32_t)table[j >> a.page_shift] < (uint32_t)a.num_pages;
+  return ok;
 }
 
 // A work-group takes 128 rows, 32 a wave, over tiles of 64 keys; K and V of the
@@ -620,38 +677,41 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
   constexpr int kTile = kPrefillKeys * C;
   __shared__ u32x4 s_k[2 * kTile], s_v[2 * kTile];
   __shared__ __attribute__((aligned(8))) uint16_t s_valid[2][4];  // keys of a tile that some query sees, 16 a wave
-  __shared__ unsigned long long s_bad;          // keys with a value that is not finite, in a tile some query sees in part
+  __shared__ int64_t s_task;
+  __shared__ int s_bad;  // a tile that some query sees in part had a value that is not finite
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n32 = lane & 31, h = lane >> 5;
-  const int64_t total = pl.row_unit[a.rows], piece = prefill_piece(total);
-  // neighbouring pieces on one XCD (work-groups go round the eight of them)
-  const int idx = (int)((blockIdx.x & 7) * (kPrefillPieces / 8) + (blockIdx.x >> 3));
-  int64_t u = idx * piece;
-  const int64_t u_end = min(u + piece, total);
+  const int64_t tasks = pl.row_task[a.rows];
   const int in_page = (1 << a.page_shift) - 1;
+  int eighth = blockIdx.x & 7, tries = 0;  // work-groups go round the eight XCDs
 
-  // this lane's share of a tile's copy: the four-key group, and per block the
-  // element offset of its chunk from the group's first key
-  const int key4 = wave * 16 + (lane >> 2 & ~3), low = lane >> 2 & 3;
-  int src_off[S];
-#pragma unroll
-  for (int b = 0; b < S; ++b) src_off[b] = (low ^ b) * D + 32 * b + 8 * ((lane & 3) ^ (key4 >> 2 & 3));
+  // this lane's share of a tile's copy: its key, and a chunk of each block
+  const int wave0 = __builtin_amdgcn_readfirstlane(wave);
+  const uint32_t to_k = lds_offset(s_k) + wave0 * 1024, to_v = lds_offset(s_v) + wave0 * 1024;
+  const int my_key = wave * 16 + (lane >> 2), my_off = 8 * ((lane & 3) ^ (lane >> 4));
   // chunks this lane multiplies
   int k_at[D / 16], v_at[S][2];
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) k_at[c] = chunk_at<6>(n32, 2 * c + h);
+  for (int c = 0; c < D / 16; ++c) k_at[c] = chunk_at<6, false>(n32, 2 * c + h);
   {
     const int x = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int d = 0; d < S; ++d)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        v_at[d][e] = chunk_at<6>(4 * h + 8 * e + (x >> 2), 4 * d + 2 * (g & 1) + ((x & 3) >> 1)) * 2 + (x & 1);
+        v_at[d][e] = chunk_at<6, false>(4 * h + 8 * e + (x >> 2), 4 * d + 2 * (g & 1) + ((x & 3) >> 1)) * 2 + (x & 1);
   }
 
-  while (u < u_end) {
-    const PrefillItem it = prefill_item(a, pl, u);
-    const int first = (int)(u - it.i0), last = (int)min(u_end - it.i0, (int64_t)it.tl.n);
+  for (;;) {
+    if (tid == 0) {
+      s_task = next_task(pl, tasks, &eighth, &tries);
+      s_bad = 0;
+    }
+    __syncthreads();
+    const int64_t task = uniform(s_task);
+    if (task < 0) return;
+    const PrefillItem it = prefill_item(a, pl, task, false);
+    const int first = it.from, last = it.to;
     const int32_t* table = a.table + (int64_t)it.row * a.width;
     const int64_t rows = (int64_t)it.n * a.group;
     const int64_t rr = (int64_t)it.tile * kPrefillRows + wave * 32 + n32;
@@ -675,35 +735,36 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
       for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    // page of this lane's key of tile i (the same for its four-key group), -1 if no query of the item sees the key
+    // page of this lane's key of tile i, -1 if no query of the item sees the key
     const auto page_of = [&](int i) {
-      const int j = (it.tl.at(i) << 6) + key4 + low;
+      const int j = (it.tl.at(i) << 6) + my_key;
       int page = -1;
-      if (j <= it.hi && (a.window == 0 || it.lo - j < a.window || j < a.sinks)) {
-        page = table[j >> a.page_shift];
-        if (page >= a.num_pages) page = -1;
-      }
-      return page;
+      if (j <= it.hi && (a.window == 0 || it.lo - j < a.window || j < a.sinks)) page = table[j >> a.page_shift];
+      return page;  // as it stands in the table: the load is not waited for here
     };
     const auto copy_tile = [&](int i, int page, int buf) {
-      const unsigned long long there = __ballot(page >= 0);
+      const bool in = (uint32_t)page < (uint32_t)a.num_pages;
+      const unsigned long long there = __ballot(in);
       if (lane == 0) s_valid[buf][wave] = every_fourth(there);
-      // the four keys of a group lie in one page; a lane copies another key of it in each block, so it
-      // needs the page where its own key is hidden, too
-      page = max(page, __shfl_xor(page, 4, 64));
-      page = max(page, __shfl_xor(page, 8, 64));
-      const int j = (it.tl.at(i) << 6) + key4;
-      const uint16_t* p = a.pool + page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D;
-#pragma unroll
-      for (int b = 0; b < S; ++b) {
-        // keys of a group change places between blocks, and with them whether they are seen
-        const bool in = (there >> ((lane & ~15) + ((low ^ b) << 2))) & 1;
-        const uint16_t* k = in ? p + src_off[b] : pl.zeros;
-        const uint16_t* v = in ? p + src_off[b] + a.plane : pl.zeros;
-        load_lds16(k, s_k + buf * kTile + b * (kPrefillKeys * 4) + wave * 64);
-        load_lds16(v, s_v + buf * kTile + b * (kPrefillKeys * 4) + wave * 64);
-      }
+      const int j = (it.tl.at(i) << 6) + my_key;
+      const uint16_t* k = a.pool + (uint32_t)page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + my_off;
+      const uint16_t* v = k + a.plane;
+      if (!in) k = v = pl.zeros;
+      const uint32_t dk = to_k + buf * (kTile * 16), dv = to_v + buf * (kTile * 16);
+      load_lds16<0>(k, dk);
+      load_lds16<64>(k, dk + 4096);
+      if (S > 2) load_lds16<128>(k, dk + 8192);
+      if (S > 3) load_lds16<192>(k, dk + 12288);
+      load_lds16<0>(v, dv);
+      load_lds16<64>(v, dv + 4096);
+      if (S > 2) load_lds16<128>(v, dv + 8192);
+      if (S > 3) load_lds16<192>(v, dv + 12288);
     };
+    const auto all_see = [&](int j0) {
+      return j0 + 63 <= it.lo && (a.window == 0 || it.hi - j0 < a.window || j0 + 63 < a.sinks);
+    };
+    const auto run_tiles = [&](auto planes) {
+    constexpr int NP = decltype(planes)::n;
     int page = page_of(first);
     copy_tile(first, page, 0);
     page = first + 1 < last ? page_of(first + 1) : -1;
@@ -712,17 +773,13 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
       const int j0 = it.tl.at(i) << 6;
       loads_done();
       __syncthreads();
-      const uint64_t valid = *reinterpret_cast<const uint64_t*>(s_valid[buf]);
+      const uint64_t valid = (uint64_t)uniform(*reinterpret_cast<const int64_t*>(s_valid[buf]));
       // every query of the item sees every key of the tile
-      const bool whole = valid == ~0ull && j0 + 63 <= it.lo &&
-                         (a.window == 0 || it.hi - j0 < a.window || j0 + 63 < a.sinks);
-      unsigned long long bad = 0;
+      const bool whole = valid == ~0ull && all_see(j0);
       if (!whole) {
         // A weight of 0 does not keep out a value that is infinite or NaN:
-        // such values leave the tile here, and are added for the queries that
-        // see them below.
-        if (tid == 0) s_bad = 0;
-        __syncthreads();
+        // such values leave the tile here, and reach the queries that see them
+        // at the item's end.
 #pragma unroll
         for (int x = 0; x < kTile / 256; ++x) {
           const int at = tid + 256 * x;
@@ -737,12 +794,10 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
               if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
             }
             s_v[buf * kTile + at] = v;
-            const int b = at / (kPrefillKeys * 4), key = ((at >> 2) & (kPrefillKeys - 1)) ^ (b & 3);
-            atomicOr(&s_bad, 1ull << key);
+            s_bad = 1;
           }
         }
         __syncthreads();
-        bad = s_bad;
       }
       if (i + 1 < last) {
         const int next = page;
@@ -750,19 +805,37 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
         copy_tile(i + 1, next, buf ^ 1);
       }
       __builtin_amdgcn_sched_barrier(0);
-      const u32x4* kt = s_k + buf * kTile;
+      const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
+      // all reads of K ahead of its products
+      u32x4 kf[D / 16][2];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c] + t * 128];
+      __builtin_amdgcn_sched_barrier(0);
       f32x16 s[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const bf16x8 k = __builtin_bit_cast(bf16x8, kt[k_at[c] + t * 128]);
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-          for (int n = NQ - 1; n >= 0; --n) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[c][n], s[t], 0, 0, 0);
-        }
-      }
+        for (int n = NQ - 1; n >= 0; --n)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[c][t]), q[c][n], s[t], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      // V of the first two key quarters while the products finish
+      bf16x8 vf[2][S];
+      const auto read_v = [&](int kc) {
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+          vf[kc & 1][d] = join_halves(read_tr(vt, (v_at[d][0] >> 1) + kc * 64, v_at[d][0] & 1),
+                                      read_tr(vt, (v_at[d][1] >> 1) + kc * 64, v_at[d][1] & 1));
+      };
+      read_v(0);
+      read_v(1);
       __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
         uint64_t seen = below(pos - j0 + 1) & valid;
@@ -781,77 +854,85 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-      top = fmaxf(top, __shfl_xor(top, 32, 64)) * pl.c;
-      if (__any(top > m)) {
+      top = max_halves(top) * pl.c;
+      // the reference follows only when it is left far behind: weights up to 2^8
+      // are as exact, and rescaling costs a pass over o
+      if (__any(top > m + 8.0f)) {
         const float mn = fmaxf(m, top);
-        const float f = exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
         m = mn;
         l *= f;
 #pragma unroll
         for (int d = 0; d < S; ++d) o[d] *= f;
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-      for (; bad != 0; bad &= bad - 1) {  // a key with a value that is not finite, for the queries that see it
-        const int key = __ffsll(bad) - 1, j = j0 + key;
-        const int at = (key >> 5) * 16 + ((key & 31) >> 3) * 4 + (key & 3);
-        float x = 0.0f;
+      bf16x8 w[2][NP];
+      const auto weights = [&](int kc) {
+        float p[8];
 #pragma unroll
-        for (int r = 0; r < 32; ++r) x = r == at ? s[r >> 4][r & 15] : x;
-        x = __shfl(x, n32 + 32 * ((key >> 2) & 1), 64);
-        const float p = __builtin_amdgcn_exp2f(fmaf(x, pl.c, -ref));
-        const uint16_t* v = a.pool + a.plane + table[j >> a.page_shift] * a.page_stride +
-                            (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + 4 * h;
+        for (int e = 0; e < 8; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(fmaf(s[kc >> 1][8 * (kc & 1) + e], pl.c, -ref));
+          if (NP > 1) l += p[e];
+        }
+        split_weights<NP>(p, w[kc & 1]);
+        if (NP == 1) {  // the sum of the rounded weights: what rounding does to all of them alike cancels
+          typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+          const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{w[kc & 1][0][2 * e], w[kc & 1][0][2 * e + 1]}, one, l, false);
+        }
+      };
+      weights(0);
+      __builtin_amdgcn_sched_barrier(0);
+      // the next quarter's weights are formed beside this one's products
+#pragma unroll
+      for (int kc = 0; kc < 4; ++kc) {
+        if (kc < 3) weights(kc + 1);
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+#pragma unroll
+          for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[kc & 1][d], w[kc & 1][n], o[d], 0, 0, 0);
+        if (kc < 2) read_v(kc + 2);
+        if (NP == 1 && kc < 3) {
+#pragma unroll
+          for (int d = 0; d < S; ++d) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a product,
+            __builtin_amdgcn_sched_group_barrier(0x402, 7, 0);  // its share of the vector work
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    };
+    if constexpr (F32) run_tiles(Planes<3>());
+    else if (few) run_tiles(Planes<2>());
+    else run_tiles(Planes<1>());
+    __syncthreads();  // the next item's first tile goes over a buffer that may still be read
+    if (s_bad) {
+      for (int j = it.tl.at(first) << 6; j <= it.hi; ++j) {
+        const int tile = j >> 6, i = tile < it.tl.head ? tile : tile - it.tl.from + it.tl.head;
+        if ((tile >= it.tl.head && tile < it.tl.from) || i < first || i >= last) continue;
+        const int page = table[j >> a.page_shift];
+        // a tile that every query saw whole kept its values
+        if ((uint32_t)page >= (uint32_t)a.num_pages || !sees(a, pos, j)) continue;
+        if (all_see(tile << 6) && tile_has_pages(a, table, tile)) continue;
+        const uint16_t* v = a.pool + a.plane + page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < S; ++d)
 #pragma unroll
           for (int r = 0; r < 16; r += 4) {
             const u32x2 y = *reinterpret_cast<const u32x2*>(v + 32 * d + 2 * r);
+            if (finite_bf16x2(y[0]) && finite_bf16x2(y[1])) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float z = bf16_bits_to_float(e & 1 ? y[e >> 1] >> 16 : y[e >> 1] & 0xffffu);
-              if (x != -INFINITY && !(fabsf(z) < INFINITY)) o[d][r + e] = fmaf(p, z, o[d][r + e]);
+              if (!(fabsf(z) < INFINITY)) o[d][r + e] += z;
             }
-            asm volatile("" ::: "memory");  // one load at a time: this is rare, and registers are not
           }
       }
-      const auto add_values = [&](auto planes) {
-        constexpr int NP = decltype(planes)::n;
-        const u32x4* vt = s_v + buf * kTile;
-#pragma unroll
-        for (int kc = 0; kc < 4; ++kc) {
-          __builtin_amdgcn_sched_barrier(0);
-          float p[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(fmaf(s[kc >> 1][8 * (kc & 1) + e], pl.c, -ref));
-            l += p[e];
-          }
-          const auto value = [&](int d) {
-            return join_halves(read_tr(vt, (v_at[d][0] >> 1) + kc * 64, v_at[d][0] & 1),
-                               read_tr(vt, (v_at[d][1] >> 1) + kc * 64, v_at[d][1] & 1));
-          };
-          bf16x8 w[NP];
-          if (!F32 && few) {
-            bf16x8 w2[2];
-            split_weights<2>(p, w2);
-#pragma unroll
-            for (int d = 0; d < S; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value(d), w2[1], o[d], 0, 0, 0);
-            w[0] = w2[0];
-          } else {
-            split_weights<NP>(p, w);
-          }
-#pragma unroll
-          for (int d = 0; d < S; ++d) {
-            const bf16x8 v = value(d);
-#pragma unroll
-            for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[n], o[d], 0, 0, 0);
-          }
-        }
-      };
-      if (F32) add_values(Planes<3>());
-      else add_values(Planes<1>());
     }
-    __syncthreads();  // the next item's first tile goes over a buffer that may still be read
+    __syncthreads();
     l += __shfl_xor(l, 32, 64);
     if (first == 0 && last == it.tl.n) {
       const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -869,7 +950,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
           }
       }
     } else {
-      const int64_t slot = (int64_t)idx * 2 + (first == 0 && u != idx * piece ? 1 : 0);
+      const int64_t slot = it.slot + it.part;
       const int r0 = wave * 32 + n32;
       float* dst = pl.part + (slot * kPrefillRows + r0) * D + 4 * h;
 #pragma unroll
@@ -882,27 +963,24 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void prefill_attn_kernel(AttnArgs
         pl.ml[(slot * 2 + 1) * kPrefillRows + r0] = l;
       }
     }
-    u = it.i0 + last;
   }
 }
 
-// Joins items cut between pieces (grid.x: cuts; grid.y: quarters of the rows),
+// Joins split items (grid.x: slots, an item's first one joins it; grid.y: quarters of the rows),
 // and clears rows whose query tile no key tile belongs to.
 template <int D>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan pl) {
   const int wave = threadIdx.x >> 6;
-  const int64_t total = pl.row_unit[a.rows], piece = prefill_piece(total);
-  const int64_t cut = ((int64_t)blockIdx.x + 1) * piece;
-  if (cut < total) {
-    const PrefillItem it = prefill_item(a, pl, cut);
-    const int64_t w0 = it.i0 / piece;
-    if (it.i0 != cut && w0 == blockIdx.x) {
-      const int64_t w1 = (it.i0 + it.tl.n - 1) / piece;
+  if (blockIdx.x < pl.row_slot[a.rows]) {
+    const PrefillItem it = prefill_item(a, pl, blockIdx.x, true);
+    if (it.part == 0) {
+      const int64_t slot = it.slot, L = pl.head[0];
+      const int parts = (int)((it.tl.n + L - 1) / L);
       for (int r = blockIdx.y * 32 + wave; r < (int)blockIdx.y * 32 + 32; r += 4) {
         const int64_t rr = (int64_t)it.tile * kPrefillRows + r;
         if (rr >= (int64_t)it.n * a.group) break;
         float o[2];
-        const float l = join_row<D, kPrefillRows>(pl, w0, w1, it.i0 != w0 * piece, r, o);
+        const float l = join_row<D, kPrefillRows>(pl, parts, r, [&](int i) { return slot + i; }, o);
         const int qi = (int)(rr / a.group), hq = it.kvh * a.group + (int)(rr - (int64_t)qi * a.group);
         store_row<D>(a, (int64_t)(it.first + qi) * a.ldo + (int64_t)hq * D, o, l);
       }
@@ -930,17 +1008,17 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan 
 }
 
 struct AttnSizes {
-  size_t part, ml, row_unit, row_tiles, tile_unit;
-  size_t all() const { return part + ml + row_unit + row_tiles + tile_unit + 256; }
+  size_t part, ml, row, tile;
+  size_t all() const { return part + ml + 3 * row + 2 * tile + 512; }
 };
 size_t up256(int64_t b) { return (size_t)((b + 255) / 256 * 256); }
 AttnSizes attn_sizes(int64_t queries, int heads_q, int64_t rows, int D) {
-  const int64_t slots = max((int64_t)kDecodePieces * kDecodeRows, (int64_t)kPrefillPieces * kPrefillRows) * 2;
+  const int64_t n = max((int64_t)kDecodePieces * 2 * kDecodeRows, (int64_t)kPrefillSlots * kPrefillRows);
   AttnSizes s;
-  s.part = up256(slots * D * 4);
-  s.ml = up256(slots * 2 * 4);
-  s.row_unit = s.row_tiles = up256((rows + 1) * 8);
-  s.tile_unit = up256((queries * heads_q / kPrefillRows + rows + 1) * 8);
+  s.part = up256(n * D * 4);
+  s.ml = up256(n * 2 * 4);
+  s.row = up256((rows + 1) * 8);
+  s.tile = up256((queries * heads_q / kPrefillRows + rows + 1) * 4);
   return s;
 }
 
@@ -957,8 +1035,8 @@ hipError_t launch(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
     return hipGetLastError();
   }
   prefill_plan_kernel<<<1, 1024, 0, s>>>(a, pl);
-  prefill_attn_kernel<D, F32><<<kPrefillPieces, 256, 0, s>>>(a, pl);
-  prefill_join_kernel<D><<<dim3(kPrefillPieces - 1, 4), 256, 0, s>>>(a, pl);
+  prefill_attn_kernel<D, F32><<<kPrefillGroups, 256, 0, s>>>(a, pl);
+  prefill_join_kernel<D><<<dim3(kPrefillSlots, 4), 256, 0, s>>>(a, pl);
   return hipGetLastError();
 }
 
@@ -974,10 +1052,14 @@ hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
   AttnPlan pl;
   pl.part = reinterpret_cast<float*>(p);
   pl.ml = reinterpret_cast<float*>(p += z.part);
-  pl.row_unit = reinterpret_cast<int64_t*>(p += z.ml);
-  pl.row_tiles = reinterpret_cast<int64_t*>(p += z.row_unit);
-  pl.tile_unit = reinterpret_cast<int64_t*>(p += z.row_tiles);
-  pl.zeros = reinterpret_cast<uint16_t*>(p += z.tile_unit);
+  pl.row_task = reinterpret_cast<int64_t*>(p += z.ml);
+  pl.row_slot = reinterpret_cast<int64_t*>(p += z.row);
+  pl.row_tiles = reinterpret_cast<int64_t*>(p += z.row);
+  pl.tile_task = reinterpret_cast<int32_t*>(p += z.row);
+  pl.tile_slot = reinterpret_cast<int32_t*>(p += z.tile);
+  pl.zeros = reinterpret_cast<uint16_t*>(p += z.tile);
+  pl.head = reinterpret_cast<int64_t*>(p += 256);
+  pl.next = reinterpret_cast<int32_t*>(p + 64);
   // t = s c with c > 0, so that the largest score has the largest t
   const float log2e = 1.4426950408889634f;
   pl.qmul = a.scale > 0.0f ? 1.0f : a.scale < 0.0f ? -1.0f : 0.0f;
