@@ -1,0 +1,246 @@
+// Shared by the decode and prefill kernels of the attention over the paged
+// key-value cache: visibility, operands, the layout of tiles in LDS, joining of
+// partial results.  attention.hip describes the method.
+#pragma once
+
+#include "kv_internal.h"
+#include "quant_core.h"
+
+namespace loopq {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+constexpr int kDecodeGroups = 512;   // work-groups of the decode launch, four pieces each
+constexpr int kDecodePieces = kDecodeGroups * 4;
+constexpr int kDecodeRows = 16;      // query heads of an item
+constexpr int kDecodeKeys = 32;      // keys of a tile
+constexpr int kPrefillGroups = 256;  // work-groups of the prefill launch
+constexpr int kPrefillSlots = 2 * kPrefillGroups;
+constexpr int kPrefillRows = 256;    // (query, head) rows of an item, at most
+constexpr int kPrefillKeys = 64;
+
+// A split item: how many parts it has and which.  One record per decode piece
+// (of the item whose first part is the piece's last) or per prefill slot (of
+// the item whose first part took it); parts is 0 where there is none.
+struct JoinRecord {
+  int32_t parts, row, item, tile;
+};
+
+// what a launch needs beside the caller's arguments
+struct AttnPlan {
+  float* part;            // partial results: [slot][rows][head_dim], then
+  float* ml;              // their m and l: [slot][2][rows]
+  JoinRecord* records;
+  int32_t* row_tiles;     // prefill: query tiles before each row, [rows + 1]
+  int32_t* row_task;      // prefill: tasks before each row, [rows + 1]
+  int32_t* row_slot;      // prefill: slots before each row, [rows + 1]
+  int32_t* tile_task;     // prefill: tasks of one key head before each query tile
+  int32_t* tile_slot;     // the same for slots
+  int32_t* head;          // prefill: {most key tiles of a task, key heads of a block}
+  int32_t* next;          // tasks handed out, of each eighth of the tasks
+  const uint16_t* zeros;  // 256 zero bytes, cleared by the plan launch
+  float c;                // |scale| log2(e), or 1 for a scale of 0
+  float qmul;             // sign of the scale: queries are taken times this
+};
+
+hipError_t launch_attn_decode(const AttnArgs& a, const AttnPlan& pl, hipStream_t s);
+hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& pl, hipStream_t s);
+
+__device__ __forceinline__ int row_len(const AttnArgs& a, int row) {
+  const int64_t cap = (int64_t)a.width << a.page_shift;
+  const int64_t n = a.lens[row];
+  return (int)(n < 0 ? 0 : n > cap ? cap : n);
+}
+
+// the row's queries: the first and their number, inside [0, queries)
+__device__ __forceinline__ int row_queries(const AttnArgs& a, int row, int* first) {
+  const int s = min(max(a.cu[row], 0), a.queries);
+  const int e = min(max(a.cu[row + 1], s), a.queries);
+  *first = s;
+  return e - s;
+}
+
+// Tiles of 2^shift keys that queries at positions lo .. hi can see: `head`
+// tiles from key 0 (sinks), then those from tile `from` on; their number.
+struct Tiles {
+  int head, from, n;
+  __device__ __forceinline__ int at(int i) const { return i < head ? i : from + i - head; }
+};
+__device__ __forceinline__ Tiles visible_tiles(const AttnArgs& a, int lo, int hi, int shift) {
+  Tiles t{0, 0, 0};
+  if (hi < 0) return t;
+  const int64_t low = a.window > 0 ? max((int64_t)lo - a.window + 1, (int64_t)0) : 0;  // first key in the window
+  t.from = (int)(low >> shift);
+  t.head = (int)min((int64_t)t.from, ((int64_t)a.sinks + (1 << shift) - 1) >> shift);
+  t.n = t.head + (hi >> shift) - t.from + 1;
+  return t;
+}
+
+// bits 0 .. n - 1
+__device__ __forceinline__ uint64_t below(int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// every fourth bit of x, 16 of them
+__device__ __forceinline__ uint16_t every_fourth(uint64_t x) {
+  x &= 0x1111111111111111ull;
+  x = (x | (x >> 3)) & 0x0303030303030303ull;
+  x = (x | (x >> 6)) & 0x000f000f000f000full;
+  x = (x | (x >> 12)) & 0x000000ff000000ffull;
+  return (uint16_t)(x | (x >> 24));
+}
+
+__device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
+  return j <= p && (a.window == 0 || p - j < a.window || j < a.sinks);
+}
+
+// the last i in [0, n) with p[i] <= u
+template <class T>
+__device__ __forceinline__ int find(const T* p, int n, T u) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// eight query elements as N bf16 planes of an MFMA operand
+template <int N>
+__device__ __forceinline__ void load_query(const AttnArgs& a, float mul, int64_t at, bool in, bf16x8 (&q)[N]) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+  if (in) {
+    if (N == 1) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + at);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = mul * bf16_bits_to_float(e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xffffu);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = mul * reinterpret_cast<const float*>(a.q)[at + e];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      q[n][e] = (__bf16)x[e];
+      x[e] -= (float)q[n][e];
+    }
+}
+
+// Eight weights as N bf16 planes: one, rounded to nearest; or the leading bits
+// cut off for all but the last, so that no plane is negative, and none 0 unless
+// the weight is (2^-126 where nothing is left): every plane times an infinite
+// value then is that infinity.
+template <int N>
+__device__ __forceinline__ void split_weights(const float (&p)[8], bf16x8 (&w)[N]) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = p[e];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    u32x4 b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      b[e] = n + 1 < N ? __builtin_amdgcn_perm(__float_as_uint(x[2 * e + 1]), __float_as_uint(x[2 * e]), 0x07060302u)
+                       : bf16x2_rne(x[2 * e], x[2 * e + 1]);
+    w[n] = __builtin_bit_cast(bf16x8, b);
+    if (n + 1 < N)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = fmaxf(x[e] - __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u), fminf(p[e], 0x1p-126f));
+  }
+}
+
+template <int N>
+struct Planes {
+  static constexpr int n = N;
+};
+
+// Place of 16-byte chunk ch of a key's row in a tile of 2^LOG keys in LDS:
+// blocks of four chunks (32 columns), the key's 64 bytes of each block in one
+// run, chunks permuted by the key: reads of one chunk of 16 keys and transposing
+// reads of four keys each spread over all banks.  ROWS also permutes the keys by
+// the block, which does the same for writes of whole rows.
+template <int LOG, bool ROWS>
+__device__ __forceinline__ int chunk_at(int key, int ch) {
+  return ((ch >> 2) << (LOG + 2)) + ((ROWS ? key ^ ((ch >> 2) & 3) : key) << 2) + ((ch & 3) ^ ((key >> 2) & 3));
+}
+
+__device__ __forceinline__ u32x2 read_tr(const u32x4* tile, int chunk, int half) {
+  const char* p = reinterpret_cast<const char*>(tile) + chunk * 16 + half * 8;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p)));
+}
+
+__device__ __forceinline__ bf16x8 join_halves(u32x2 x, u32x2 y) {
+  return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int64_t at, const float (&o)[2], float l) {
+  const int lane = threadIdx.x & 63;
+  const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int d = lane + 64 * h;
+    if (d >= D) break;
+    if (a.bf16) reinterpret_cast<uint16_t*>(a.out)[at + d] = (uint16_t)bf16x2_rne(o[h] * f, 0.0f);
+    else reinterpret_cast<float*>(a.out)[at + d] = o[h] * f;
+  }
+}
+
+// Parts first, first + step, ... of n of one row, one wave: columns lane and
+// lane + 64 of the sum at the reference m of all n parts, and l.
+template <int D, int ROWS, class F>
+__device__ __forceinline__ float join_parts(const AttnPlan& pl, int n, int first, int step, int r, F slot_of, float (&o)[2]) {
+  const int lane = threadIdx.x & 63;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 64) m = fmaxf(m, pl.ml[slot_of(i) * 2 * ROWS + r]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  o[0] = o[1] = 0.0f;
+#pragma unroll 8
+  for (int i = first; i < n; i += step) {
+    const int64_t slot = slot_of(i);
+    const float f = __builtin_amdgcn_exp2f(pl.ml[slot * 2 * ROWS + r] - ref);
+    const float* p = pl.part + (slot * ROWS + r) * D;
+    l = fmaf(f, pl.ml[(slot * 2 + 1) * ROWS + r], l);
+    o[0] = fmaf(f, p[lane], o[0]);
+    if (D > 64) o[1] = fmaf(f, lane + 64 < D ? p[lane + 64] : 0.0f, o[1]);
+  }
+  return l;
+}
+
+// The records among n that stand for an item, into `list` in their order (the
+// same in every work-group); their number.  256 threads, ends with a barrier.
+__device__ __forceinline__ int split_items(const JoinRecord* records, int n, int* list) {
+  __shared__ int count[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int i0 = 0; i0 < n; i0 += 256) {
+    const int i = i0 + tid;
+    const uint64_t is = __ballot(i < n && records[i].parts > 0);
+    if (lane == 0) count[wave] = __popcll(is);
+    __syncthreads();
+    int at = base;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      at += w < wave ? count[w] : 0;
+      base += count[w];
+    }
+    if ((is >> lane) & 1) list[at + __popcll(is & ((1ull << lane) - 1))] = i;
+    __syncthreads();
+  }
+  return base;
+}
+
+}  // namespace loopq

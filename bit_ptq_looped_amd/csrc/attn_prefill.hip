@@ -1,0 +1,615 @@
+// Attention of several new tokens a row over the paged cache, causal, with a
+// sliding window and sinks (attention.hip has the method).
+#include "attn_core.h"
+
+namespace loopq {
+namespace {
+
+// Rows of a query tile are (query, head of the group) pairs, heads fastest.
+template <int ROWS>
+__device__ __forceinline__ int query_tiles(const AttnArgs& a, int n) {
+  return (int)(((int64_t)n * a.group + ROWS - 1) / ROWS);
+}
+template <int ROWS>
+__device__ __forceinline__ Tiles tile_keys(const AttnArgs& a, int t, int n, int len, int* lo, int* hi) {
+  const int64_t r0 = (int64_t)t * ROWS, r1 = min(r0 + ROWS, (int64_t)n * a.group) - 1;
+  *lo = len - n + (int)(r0 / a.group);
+  *hi = len - n + (int)(r1 / a.group);
+  return visible_tiles(a, *lo, *hi, 6);
+}
+
+// the larger of lanes x and x + 32, in both
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The last i in [0, n) with p[i] <= x (p[0] <= x, p ascending), by the whole
+// wave: 64 places at a time, since a place costs a trip to memory.
+__device__ __forceinline__ int find_wave(const int32_t* p, int n, int x) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, step;
+  do {
+    step = (n - lo + 63) >> 6;
+    const int i = lo + lane * step;
+    const int below = __popcll(__ballot(i < n && p[min(i, n - 1)] <= x)) - 1;
+    lo += below * step;
+    n = min(n, lo + step);
+  } while (step > 1);
+  return lo;
+}
+
+// exclusive sum over 1024 threads, and the sum of all; `part` is 16 values of scratch
+__device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* part, int64_t* all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t x = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) part[wave] = x;
+  __syncthreads();
+  int64_t before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    before += w < wave ? part[w] : 0;
+    sum += part[w];
+  }
+  *all = sum;
+  return before + x - v;
+}
+
+// One work-group.  A task is an item or, where an item has more than L key
+// tiles, a part of it of at most L; L is a work-group's even share of all key
+// tiles, so that few long items are split over the whole chip and many stay
+// whole.  Slots take the results of split items' tasks: at most 2 tiles / L.
+template <int ROWS>
+__global__ __launch_bounds__(1024) void prefill_plan_kernel(AttnArgs a, AttnPlan pl) {
+  __shared__ int64_t part[16];
+  __shared__ int32_t s_rows[1025];
+  const int tid = threadIdx.x;
+  if (tid < 64) reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(pl.zeros))[tid] = 0;
+  if (tid < 8) pl.next[tid] = 0;
+  int64_t T = 0, all;
+  for (int r0 = 0; r0 < a.rows; r0 += 1024) {
+    const int r = r0 + tid;
+    int first;
+    const int n = r < a.rows ? query_tiles<ROWS>(a, row_queries(a, r, &first)) : 0;
+    const int64_t at = T + sum_before(n, part, &all);
+    if (r < a.rows) {
+      pl.row_tiles[r] = (int32_t)at;
+      if (r < 1024) s_rows[r] = (int32_t)at;
+    }
+    T += all;
+  }
+  if (tid == 0) {
+    pl.row_tiles[a.rows] = (int32_t)T;
+    if (a.rows < 1025) s_rows[a.rows] = (int32_t)T;
+  }
+  __syncthreads();
+  const int32_t* row_tiles = a.rows <= 1024 ? s_rows : pl.row_tiles;
+  const auto keys_of = [&](int t) {
+    const int row = find(row_tiles, a.rows, t);
+    int first, lo, hi;
+    const int n = row_queries(a, row, &first);
+    return tile_keys<ROWS>(a, t - row_tiles[row], n, row_len(a, row), &lo, &hi).n;
+  };
+  int64_t keys = 0;
+  int mine = 0;  // key tiles of query tile tid: most calls have no more than 1024
+  for (int64_t t = tid; t < T; t += 1024) {
+    const int n = keys_of((int)t);
+    if (t < 1024) mine = n;
+    keys += n;
+  }
+  sum_before(keys, part, &all);
+  const int64_t L = max((int64_t)4, (all * a.heads + kPrefillGroups - 1) / kPrefillGroups);
+  int64_t base = 0;  // tasks in the low half, slots in the high one
+  for (int64_t t0 = 0; t0 < T; t0 += 1024) {
+    const int64_t t = t0 + tid;
+    const int64_t n = t < T ? (t < 1024 ? mine : keys_of((int)t)) : 0, parts = (n + L - 1) / L;
+    const int64_t at = base + sum_before(parts + (parts > 1 ? parts << 32 : 0), part, &all);
+    if (t < T) {
+      pl.tile_task[t] = (int32_t)at;
+      pl.tile_slot[t] = (int32_t)(at >> 32);
+    }
+    base += all;
+  }
+  __syncthreads();
+  for (int r = tid; r <= a.rows; r += 1024) {
+    const int t = r < a.rows ? row_tiles[r] : (int)T;
+    pl.row_task[r] = a.heads * (t < T ? pl.tile_task[t] : (int32_t)base);
+    pl.row_slot[r] = a.heads * (t < T ? pl.tile_slot[t] : (int32_t)(base >> 32));
+  }
+  if (tid == 0) {
+    pl.head[0] = (int32_t)min(L, (int64_t)0x7fffffff);
+    pl.head[1] = min(max(a.heads * a.rows / 8, 1), a.heads);
+  }
+}
+
+struct PrefillItem {
+  int row, kvh, tile, part, parts, n, len, first;  // first: the row's first query
+  int lo, hi;                                      // positions of the tile's queries
+  Tiles tl;
+  int from, to;                                    // key tiles of the task
+  int slot;                                        // of the item's first task, if there are several
+};
+// Task x.  A row's key heads come in blocks, as many as share an XCD; in a block
+// the query tiles go from the last, which has the most keys, to the first, each
+// for every head: work-groups that run together read the same keys, and what is
+// handed out at the end is short.
+template <int ROWS>
+__device__ __forceinline__ PrefillItem prefill_item(const AttnArgs& a, const AttnPlan& pl, int x) {
+  PrefillItem it;
+  it.row = find_wave(pl.row_task, a.rows, x);
+  it.n = row_queries(a, it.row, &it.first);
+  it.len = row_len(a, it.row);
+  const int L = pl.head[0], block = pl.head[1];
+  const int t0 = pl.row_tiles[it.row], t1 = pl.row_tiles[it.row + 1];
+  const int task0 = pl.row_task[it.row], per = (pl.row_task[it.row + 1] - task0) / a.heads;
+  const int slot0 = pl.row_slot[it.row], slots = (pl.row_slot[it.row + 1] - slot0) / a.heads;
+  x -= task0;
+  const int b = x / (block * per), heads = min(block, a.heads - b * block);
+  x -= b * block * per;
+  const int y = x / heads;
+  it.kvh = b * block + x - y * heads;
+  const int z = task0 / a.heads + per - 1 - y;
+  it.tile = find_wave(pl.tile_task + t0, t1 - t0, z);
+  it.part = z - pl.tile_task[t0 + it.tile];
+  it.slot = slot0 + it.kvh * slots + pl.tile_slot[t0 + it.tile] - slot0 / a.heads;
+  it.tl = tile_keys<ROWS>(a, it.tile, it.n, it.len, &it.lo, &it.hi);
+  it.parts = (int)(((int64_t)it.tl.n + L - 1) / L);
+  it.from = (int)((int64_t)it.part * L);
+  it.to = (int)min(((int64_t)it.part + 1) * L, (int64_t)it.tl.n);
+  return it;
+}
+
+// 16 bytes per lane from src + OFF (bytes, per lane) to LDS at byte dst + 16
+// lane (dst a scalar), without passing the registers.  The compiler does not see
+// the write: a reader waits for loads_done() and the barrier after it.  The
+// offset counts for the target, too; one wait state lies between the write of
+// m0 and its use.
+template <int OFF>
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(dst - OFF), "v"(src), "n"(OFF)
+               : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+// all but the wave's last N vector memory operations are done
+template <int N>
+__device__ __forceinline__ void loads_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
+  return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
+}
+
+// whether every key of a tile of 64 has a page
+__device__ __forceinline__ bool tile_has_pages(const AttnArgs& a, const int32_t* table, int tile) {
+  bool ok = true;
+  for (int j = tile << 6; j < (tile + 1) << 6; j += min(64, 1 << a.page_shift))
+    ok &= (uint32_t)table[j >> a.page_shift] < (uint32_t)a.num_pages;
+  return ok;
+}
+
+// A work-group takes a task after another: W waves of 32 rows each over tiles of
+// 64 keys, K and V of the next two tiles on their way to a ring of three buffers
+// in LDS while one is multiplied.  Keys that no query of the item sees are read
+// from a line of zeros.  fp32 queries hold three planes in registers and take
+// half the rows.
+template <int D, bool F32, int W>
+__global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a, AttnPlan pl) {
+  constexpr int NQ = F32 ? 3 : 1;
+  constexpr int ROWS = 32 * W, THREADS = 64 * W;
+  constexpr int C = D / 8, S = D / 32;  // chunks and blocks of a row
+  constexpr int kTile = kPrefillKeys * C;
+  constexpr int kCopies = 8 * S / W;  // of a wave for one tile
+  __shared__ u32x4 s_k[3 * kTile], s_v[3 * kTile];
+  __shared__ __attribute__((aligned(8))) uint16_t s_valid[3][4];  // keys of a tile that some query sees, 16 a wave
+  __shared__ int s_pages[512];  // of 64 tiles' groups of eight keys
+  __shared__ int s_task;
+  __shared__ int s_bad;  // a tile that some query sees in part had a value that is not finite
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n32 = lane & 31, h = lane >> 5;
+  const int in_page = (1 << a.page_shift) - 1;
+  const int64_t tasks = pl.row_task[a.rows];
+  // Work-groups go round the eight XCDs; each XCD has an eighth of the tasks
+  // (neighbours share keys, and with them an L2), a first one per work-group and
+  // the rest in turn, then helps out in the other eighths.  Which work-group
+  // takes a task does not change its result.
+  constexpr int kPer = kPrefillGroups / 8;
+  const int eighth = blockIdx.x & 7;
+  const auto start_of = [&](int e) { return (int)(tasks * e / 8); };
+  int task = start_of(eighth) + (int)(blockIdx.x >> 3);
+  if (task >= start_of(eighth + 1)) task = -1;
+
+  // this lane's share of a tile's copy: its key, and a chunk of each block
+  const int wave0 = __builtin_amdgcn_readfirstlane(wave);
+  const int my_key = (wave0 & 3) * 16 + (lane >> 2), my_off = 8 * ((lane & 3) ^ (lane >> 4));
+  const uint32_t to_k = lds_offset(s_k) + (wave0 & 3) * 1024, to_v = lds_offset(s_v) + (wave0 & 3) * 1024;
+  // chunks this lane multiplies
+  int k_at[D / 16], v_at[S][2];
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) k_at[c] = chunk_at<6, false>(n32, 2 * c + h);
+  {
+    const int x = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int d = 0; d < S; ++d)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        v_at[d][e] = chunk_at<6, false>(4 * h + 8 * e + (x >> 2), 4 * d + 2 * (g & 1) + ((x & 3) >> 1)) * 2 + (x & 1);
+  }
+
+  for (;;) {
+    if (task < 0 && wave0 == 0) {  // what the other eighths have left
+      int found = -1;
+      uint64_t open = 0xff;  // a try that fails closes an eighth for good: nine rounds at most
+      for (;;) {
+        const int e = (eighth + lane) & 7;
+        const int left = max(start_of(e + 1) - start_of(e) - kPer, 0);
+        const int taken = __hip_atomic_load(pl.next + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        open &= __ballot(lane < 8 && taken < left);
+        if (open == 0) break;
+        const int at = __ffsll((unsigned long long)open) - 1, f = (eighth + at) & 7;
+        int x = lane == 0 ? atomicAdd(pl.next + f, 1) : 0;
+        x = __builtin_amdgcn_readfirstlane(x);
+        if (x < start_of(f + 1) - start_of(f) - kPer) {
+          found = start_of(f) + kPer + x;
+          break;
+        }
+        open &= ~(1ull << at);
+      }
+      if (lane == 0) s_task = found;
+    }
+    if (task < 0) {
+      __syncthreads();
+      task = __builtin_amdgcn_readfirstlane(s_task);
+      if (task < 0) return;
+    }
+    if (tid == 0) s_bad = 0;
+    const PrefillItem it = prefill_item<ROWS>(a, pl, task);
+    const int first = it.from, last = it.to;
+    // the eighth's next task, while this one runs
+    const int own_left = start_of(eighth + 1) - start_of(eighth) - kPer;
+    int next_task = -1;
+    if (tid == 0 && own_left > 0) {
+      const int x = atomicAdd(pl.next + eighth, 1);
+      if (x < own_left) next_task = start_of(eighth) + kPer + x;
+    }
+    const int32_t* table = a.table + (int64_t)it.row * a.width;
+    const int64_t rows = (int64_t)it.n * a.group;
+    const int64_t rr = (int64_t)it.tile * ROWS + wave * 32 + n32;
+    const bool busy = (int64_t)it.tile * ROWS + wave0 * 32 < rows;  // the wave has rows
+    const bool has = rr < rows;
+    const int64_t rq = has ? rr : rows - 1;
+    const int qi = (int)(rq / a.group), hq = it.kvh * a.group + (int)(rq - (int64_t)qi * a.group);
+    const int pos = it.len - it.n + qi;  // position of this lane's query
+    // bf16 weights are rounded by up to 2^-8 of themselves; over many keys that
+    // averages out, with few the weights take a second plane
+    const bool few = !F32 && (it.lo < 255 || (a.window > 0 && a.window < 256));
+
+    bf16x8 q[D / 16][NQ];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      load_query<NQ>(a, pl.qmul, (int64_t)(it.first + qi) * a.ldq + (int64_t)hq * D + 16 * c + 8 * h, true, q[c]);
+
+    f32x16 o[S];
+#pragma unroll
+    for (int d = 0; d < S; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+
+    // pages of the keys of tiles i .. i + 63, eight keys a page at least
+    const auto read_pages = [&](int i) {
+      for (int e = tid; e < 512; e += THREADS) {
+        const int t = i + (e >> 3);
+        int page = -1;
+        if (t < last) {
+          const int j = (it.tl.at(t) << 6) + 8 * (e & 7);
+          if (j <= it.hi) page = table[j >> a.page_shift];
+        }
+        s_pages[e] = page;
+      }
+    };
+    const auto copy_tile = [&](int i, int buf) {
+      const int j = (it.tl.at(i) << 6) + my_key, page = s_pages[((i - first) & 63) * 8 + (my_key >> 3)];
+      const bool in = (uint32_t)page < (uint32_t)a.num_pages && j <= it.hi &&
+                      (a.window == 0 || it.lo - j < a.window || j < a.sinks);
+      if (wave0 < 4) {
+        const unsigned long long there = __ballot(in);
+        if (lane == 0) s_valid[buf][wave0] = every_fourth(there);
+      }
+      const uint16_t* k = a.pool + (uint32_t)page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + my_off;
+      const auto copy = [&](const uint16_t* p, uint32_t dst) {
+        if (!in) p = pl.zeros;
+        dst += buf * (kTile * 16);
+        load_lds16<0>(p, dst);
+        load_lds16<64>(p, dst + 4096);
+        if (S > 2) load_lds16<128>(p, dst + 8192);
+        if (S > 3) load_lds16<192>(p, dst + 12288);
+      };
+      if (W == 4) {
+        copy(k, to_k);
+        copy(k + a.plane, to_v);
+      } else {
+        copy(wave0 < 4 ? k : k + a.plane, wave0 < 4 ? to_k : to_v);
+      }
+    };
+    const auto all_see = [&](int j0) {
+      return j0 + 63 <= it.lo && (a.window == 0 || it.hi - j0 < a.window || j0 + 63 < a.sinks);
+    };
+    const auto run_tiles = [&](auto planes) {
+    constexpr int NP = decltype(planes)::n;
+    read_pages(first);
+    __syncthreads();
+    copy_tile(first, 0);
+    if (first + 1 < last) copy_tile(first + 1, 1);
+    int buf = 0;
+    for (int i = first; i < last; ++i, buf = buf == 2 ? 0 : buf + 1) {
+      const int j0 = it.tl.at(i) << 6;
+      // tile i is here; from the second tile on nothing but the next one's copies is under way
+      if (i > first && i + 1 < last) loads_done<kCopies>();
+      else loads_done<0>();
+      __syncthreads();
+      const u32x2 v2 = *reinterpret_cast<const u32x2*>(s_valid[buf]);
+      const uint64_t valid = ((uint64_t)__builtin_amdgcn_readfirstlane(v2[1]) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(v2[0]);
+      // every query of the item sees every key of the tile
+      const bool whole = valid == ~0ull && all_see(j0);
+      if (!whole) {
+        // A weight of 0 does not keep out a value that is infinite or NaN:
+        // such values leave the tile here, and reach the queries that see them
+        // at the item's end.
+        for (int at = tid; at < kTile; at += THREADS) {
+          u32x4 v = s_v[buf * kTile + at];
+          bool fix = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) fix |= !finite_bf16x2(v[e]);
+          if (fix) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
+              if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
+            }
+            s_v[buf * kTile + at] = v;
+            s_bad = 1;
+          }
+        }
+        __syncthreads();
+      }
+      if (i + 2 < last) {
+        if (((i + 2 - first) & 63) == 0) {
+          read_pages(i + 2);
+          __syncthreads();
+        }
+        copy_tile(i + 2, buf == 0 ? 2 : buf - 1);
+      }
+      if (!busy) continue;
+      __builtin_amdgcn_sched_barrier(0);
+      const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
+      // all reads of K ahead of its products
+      u32x4 kf[D / 16][2];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c] + t * 128];
+      __builtin_amdgcn_sched_barrier(0);
+      f32x16 s[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int n = NQ - 1; n >= 0; --n)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[c][t]), q[c][n], s[t], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      // V of the first two key quarters while the products finish
+      bf16x8 vf[2][S];
+      const auto read_v = [&](int kc) {
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+          vf[kc & 1][d] = join_halves(read_tr(vt, (v_at[d][0] >> 1) + kc * 64, v_at[d][0] & 1),
+                                      read_tr(vt, (v_at[d][1] >> 1) + kc * 64, v_at[d][1] & 1));
+      };
+      read_v(0);
+      read_v(1);
+      mfma_settle_before_join();
+      __builtin_amdgcn_sched_barrier(0);
+      if (!whole) {
+        uint64_t seen = below(pos - j0 + 1) & valid;
+        if (a.window > 0) seen &= ~below((int64_t)pos - a.window + 1 - j0) | below((int64_t)a.sinks - j0);
+        seen >>= 4 * h;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t w = (uint32_t)(seen >> (32 * t));
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (!(w & (1u << (8 * (r >> 2) + (r & 3))))) s[t][r] = -INFINITY;
+        }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+      top = max_halves(top) * pl.c;
+      // the reference follows only when it is left far behind: weights up to 2^8
+      // are as exact, and rescaling costs a pass over o
+      if (__any(top > m + 8.0f)) {
+        const float mn = fmaxf(m, top);
+        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < S; ++d) o[d] *= f;
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      bf16x8 w[2][NP];
+      const auto weights = [&](int kc) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(fmaf(s[kc >> 1][8 * (kc & 1) + e], pl.c, -ref));
+          if (NP > 1) l += p[e];
+        }
+        split_weights<NP>(p, w[kc & 1]);
+        if (NP == 1) {  // the sum of the rounded weights: what rounding does to all of them alike cancels
+          typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+          const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{w[kc & 1][0][2 * e], w[kc & 1][0][2 * e + 1]}, one, l, false);
+        }
+      };
+      weights(0);
+      __builtin_amdgcn_sched_barrier(0);
+      // the next quarter's weights are formed beside this one's products
+#pragma unroll
+      for (int kc = 0; kc < 4; ++kc) {
+        if (kc < 3) weights(kc + 1);
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+#pragma unroll
+          for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[kc & 1][d], w[kc & 1][n], o[d], 0, 0, 0);
+        if (kc < 2) read_v(kc + 2);
+        if (NP == 1 && kc < 3) {
+#pragma unroll
+          for (int d = 0; d < S; ++d) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a product,
+            __builtin_amdgcn_sched_group_barrier(0x402, 7, 0);  // its share of the vector work
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    };
+    if constexpr (F32) run_tiles(Planes<3>());
+    else if (few) run_tiles(Planes<2>());
+    else run_tiles(Planes<1>());
+    mfma_settle_before_join();
+    if (tid == 0) s_task = next_task;
+    __syncthreads();  // the next item's first tile goes over a buffer that may still be read
+    task = __builtin_amdgcn_readfirstlane(s_task);
+    if (s_bad) {
+      for (int j = it.tl.at(first) << 6; j <= it.hi; ++j) {
+        const int tile = j >> 6, i = tile < it.tl.head ? tile : tile - it.tl.from + it.tl.head;
+        if ((tile >= it.tl.head && tile < it.tl.from) || i < first || i >= last) continue;
+        const int page = table[j >> a.page_shift];
+        // a tile that every query saw whole kept its values
+        if ((uint32_t)page >= (uint32_t)a.num_pages || !sees(a, pos, j)) continue;
+        if (all_see(tile << 6) && tile_has_pages(a, table, tile)) continue;
+        const uint16_t* v = a.pool + a.plane + page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const u32x2 y = *reinterpret_cast<const u32x2*>(v + 32 * d + 2 * r);
+            if (finite_bf16x2(y[0]) && finite_bf16x2(y[1])) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float z = bf16_bits_to_float(e & 1 ? y[e >> 1] >> 16 : y[e >> 1] & 0xffffu);
+              if (!(fabsf(z) < INFINITY)) o[d][r + e] += z;
+            }
+          }
+      }
+    }
+    __syncthreads();
+    l += __shfl_xor(l, 32, 64);
+    if (it.parts == 1) {
+      const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      if (has) {
+        const int64_t at = (int64_t)(it.first + qi) * a.ldo + (int64_t)hq * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const f32x4 v = f32x4{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * f;
+            if (a.bf16)
+              *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at + 32 * d + 2 * r) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+            else
+              *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at + 32 * d + 2 * r) = v;
+          }
+      }
+    } else if (busy) {
+      const int64_t slot = it.slot + it.part;
+      if (tid == 0) pl.records[slot] = JoinRecord{it.part == 0 ? it.parts : 0, it.row, it.kvh, it.tile};
+      const int r0 = wave * 32 + n32;
+      float* dst = pl.part + (slot * ROWS + r0) * D + 4 * h;
+#pragma unroll
+      for (int d = 0; d < S; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<f32x4*>(dst + 32 * d + 2 * r) = f32x4{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]};
+      if (h == 0) {
+        pl.ml[slot * 2 * ROWS + r0] = m;
+        pl.ml[(slot * 2 + 1) * ROWS + r0] = l;
+      }
+    }
+  }
+}
+
+// Joins split items, a wave per row, and clears rows whose query tile no key
+// tile belongs to.
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan pl) {
+  __shared__ int s_list[kPrefillSlots];
+  const int wave = threadIdx.x >> 6, waves = gridDim.x * 4, me = blockIdx.x * 4 + wave;
+  const int n = split_items(pl.records, pl.row_slot[a.rows], s_list);
+  for (int x = me; x < n * ROWS; x += waves) {
+    const int slot = s_list[x / ROWS], r = x % ROWS;
+    const JoinRecord rec = pl.records[slot];
+    int first;
+    const int64_t rows = (int64_t)row_queries(a, rec.row, &first) * a.group, rr = (int64_t)rec.tile * ROWS + r;
+    if (rr >= rows) continue;
+    float o[2];
+    const float l = join_parts<D, ROWS>(pl, rec.parts, 0, 1, r, [&](int i) { return (int64_t)slot + i; }, o);
+    const int qi = (int)(rr / a.group), hq = rec.item * a.group + (int)(rr - (int64_t)qi * a.group);
+    store_row<D>(a, (int64_t)(first + qi) * a.ldo + (int64_t)hq * D, o, l);
+  }
+  // queries at negative positions whose whole tile sees nothing
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    int first;
+    const int n = row_queries(a, row, &first), len = row_len(a, row);
+    if (n <= len) continue;
+    for (int t = 0; t < query_tiles<ROWS>(a, n); ++t) {
+      int lo, hi;
+      if (tile_keys<ROWS>(a, t, n, len, &lo, &hi).n > 0) break;
+      const int64_t r1 = min(((int64_t)t + 1) * ROWS, (int64_t)n * a.group);
+      for (int64_t r = (int64_t)t * ROWS + wave; r < r1; r += 4) {
+        const int qi = (int)(r / a.group), g = (int)(r - (int64_t)qi * a.group);
+        const float z[2] = {0.0f, 0.0f};
+        for (int kvh = 0; kvh < a.heads; ++kvh)
+          store_row<D>(a, (int64_t)(first + qi) * a.ldo + (int64_t)(kvh * a.group + g) * D, z, 0.0f);
+      }
+    }
+  }
+}
+
+template <int D, bool F32>
+hipError_t launch(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+  constexpr int W = F32 ? 4 : 8;
+  prefill_plan_kernel<32 * W><<<1, 1024, 0, s>>>(a, pl);
+  prefill_attn_kernel<D, F32, W><<<kPrefillGroups, 64 * W, 0, s>>>(a, pl);
+  prefill_join_kernel<D, 32 * W><<<512, 256, 0, s>>>(a, pl);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+  switch (a.head_dim) {
+    case 64: return a.bf16 ? launch<64, false>(a, pl, s) : launch<64, true>(a, pl, s);
+    case 96: return a.bf16 ? launch<96, false>(a, pl, s) : launch<96, true>(a, pl, s);
+    default: return a.bf16 ? launch<128, false>(a, pl, s) : launch<128, true>(a, pl, s);
+  }
+}
+
+}  // namespace loopq

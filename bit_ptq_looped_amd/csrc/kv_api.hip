@@ -111,6 +111,8 @@ int32_t run_attn(const loopq_kv_pool* pool, int32_t slab, const loopq_kv_table* 
   if (queries < 0 || heads_q <= 0 || window < 0 || sinks < 0 || !isfinite(scale)) return LOOPQ_ERR_INVALID_ARG;
   if (heads_q % pool->heads || (int64_t)heads_q * pool->head_dim > (1 << 20)) return LOOPQ_ERR_UNSUPPORTED;
   if (queries == 0 || table->rows == 0) return LOOPQ_OK;
+  // query tiles of every head are counted in 32 bits
+  if ((int64_t)queries * heads_q / 128 + (int64_t)table->rows * heads_q > (1 << 30)) return LOOPQ_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)heads_q * pool->head_dim;
   st = check_rows(q, ldq, width, queries, dtype);
   if (st == LOOPQ_OK) st = check_rows(out, ldo, width, queries, dtype);
