@@ -229,7 +229,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
 
   // this lane's share of a tile's copy: its key, and a chunk of each block
   const int wave0 = __builtin_amdgcn_readfirstlane(wave);
-  const int my_key = (wave0 & 3) * 16 + (lane >> 2), my_off = 8 * ((lane & 3) ^ (lane >> 4));
+  const int my_key = (wave0 & 3) * 16 + (lane >> 2);
+  const uint32_t my_off = (my_key & in_page) * (2 * D) + 16 * ((lane & 3) ^ (lane >> 4)), page_bytes = (uint32_t)(2 * a.page_stride);
   const uint32_t to_k = lds_offset(s_k) + (wave0 & 3) * 1024, to_v = lds_offset(s_v) + (wave0 & 3) * 1024;
   // chunks this lane multiplies
   int k_at[D / 16], v_at[S][2];
@@ -316,29 +317,42 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         s_pages[e] = page;
       }
     };
-    const auto copy_tile = [&](int i, int buf) {
-      const int j = (it.tl.at(i) << 6) + my_key, page = s_pages[((i - first) & 63) * 8 + (my_key >> 3)];
-      const bool in = (uint32_t)page < (uint32_t)a.num_pages && j <= it.hi &&
-                      (a.window == 0 || it.lo - j < a.window || j < a.sinks);
-      if (wave0 < 4) {
+    // where this wave's copies of tile i come from: K and V with four waves, one of
+    // them with eight; past the last tile, zeros (so that the loop needs no branch)
+    struct Source {
+      const char *k, *v;
+    };
+    const char* head = reinterpret_cast<const char*>(a.pool + (((int64_t)it.kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0));
+    const auto page_of = [&](int i) { return s_pages[((i - first) & 63) * 8 + (my_key >> 3)]; };
+    const auto source_of = [&](int i, int buf, int page) {
+      const int j0 = it.tl.at(i) << 6, j = j0 + my_key;
+      bool in = (uint32_t)page < (uint32_t)a.num_pages;
+      if (i >= last || j0 + 63 > it.hi || (a.window > 0 && it.lo - j0 >= a.window && j0 + 63 >= a.sinks))
+        in = in && i < last && j <= it.hi && (a.window == 0 || it.lo - j < a.window || j < a.sinks);
+      if (W == 4 || wave0 < 4) {
         const unsigned long long there = __ballot(in);
-        if (lane == 0) s_valid[buf][wave0] = every_fourth(there);
+        uint16_t keys = 0xffff;
+        if (there != ~0ull) keys = every_fourth(there);
+        if (lane == 0) s_valid[buf][wave0] = keys;
       }
-      const uint16_t* k = a.pool + (uint32_t)page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + my_off;
-      const auto copy = [&](const uint16_t* p, uint32_t dst) {
-        if (!in) p = pl.zeros;
-        dst += buf * (kTile * 16);
-        load_lds16<0>(p, dst);
-        load_lds16<64>(p, dst + 4096);
-        if (S > 2) load_lds16<128>(p, dst + 8192);
-        if (S > 3) load_lds16<192>(p, dst + 12288);
+      // a page is at least eight keys long, and a tile starts one or lies in one
+      const char* p = head + (int64_t)(j0 & in_page) * (2 * D) + (uint64_t)(uint32_t)page * page_bytes + my_off;
+      const char* zero = reinterpret_cast<const char*>(pl.zeros);
+      Source x;
+      x.k = in ? p : zero;
+      x.v = W == 4 && in ? p + 2 * a.plane : zero;
+      return x;
+    };
+    const auto copy_block = [&](const Source& x, int buf, int b) {  // b a constant once unrolled
+      const uint32_t at = buf * (kTile * 16) + b * 4096;
+      const auto go = [&](const char* p, uint32_t dst) {
+        if (b == 0) load_lds16<0>(p, dst);
+        else if (b == 1) load_lds16<64>(p, dst);
+        else if (b == 2) load_lds16<128>(p, dst);
+        else load_lds16<192>(p, dst);
       };
-      if (W == 4) {
-        copy(k, to_k);
-        copy(k + a.plane, to_v);
-      } else {
-        copy(wave0 < 4 ? k : k + a.plane, wave0 < 4 ? to_k : to_v);
-      }
+      go(x.k, (W == 8 && wave0 >= 4 ? to_v : to_k) + at);
+      if (W == 4) go(x.v, to_v + at);
     };
     const auto all_see = [&](int j0) {
       return j0 + 63 <= it.lo && (a.window == 0 || it.hi - j0 < a.window || j0 + 63 < a.sinks);
@@ -347,16 +361,51 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     constexpr int NP = decltype(planes)::n;
     read_pages(first);
     __syncthreads();
-    copy_tile(first, 0);
-    if (first + 1 < last) copy_tile(first + 1, 1);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const Source x = source_of(first + t, t, page_of(first + t));
+#pragma unroll
+      for (int b = 0; b < S; ++b) copy_block(x, t, b);
+    }
     int buf = 0;
     for (int i = first; i < last; ++i, buf = buf == 2 ? 0 : buf + 1) {
       const int j0 = it.tl.at(i) << 6;
-      // tile i is here; from the second tile on nothing but the next one's copies is under way
-      if (i > first && i + 1 < last) loads_done<kCopies>();
+      const int after = buf == 0 ? 2 : buf - 1;  // the buffer that tile i + 2 goes to, free since the last barrier
+      // tile i is here: from the second one on only the copies of the next are under way
+      if (i > first) loads_done<kCopies>();
       else loads_done<0>();
       __syncthreads();
+      if (i + 2 < last && ((i + 2 - first) & 63) == 0) {
+        read_pages(i + 2);
+        __syncthreads();
+      }
       const u32x2 v2 = *reinterpret_cast<const u32x2*>(s_valid[buf]);
+      const int page = page_of(i + 2);
+      __builtin_amdgcn_sched_barrier(0);
+      const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
+      f32x16 s[2];
+      if (busy) {
+        // all reads of K ahead of its products
+        u32x4 kf[D / 16][2];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c] + t * 128];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int n = NQ - 1; n >= 0; --n)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[c][t]), q[c][n], s[t], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      mfma_settle_before_join();
       const uint64_t valid = ((uint64_t)__builtin_amdgcn_readfirstlane(v2[1]) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(v2[0]);
       // every query of the item sees every key of the tile
       const bool whole = valid == ~0ull && all_see(j0);
@@ -381,36 +430,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         }
         __syncthreads();
       }
-      if (i + 2 < last) {
-        if (((i + 2 - first) & 63) == 0) {
-          read_pages(i + 2);
-          __syncthreads();
-        }
-        copy_tile(i + 2, buf == 0 ? 2 : buf - 1);
+      const Source src = source_of(i + 2, after, page);
+      if (!busy) {
+#pragma unroll
+        for (int b = 0; b < S; ++b) copy_block(src, after, b);
+        continue;
       }
-      if (!busy) continue;
-      __builtin_amdgcn_sched_barrier(0);
-      const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
-      // all reads of K ahead of its products
-      u32x4 kf[D / 16][2];
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c] + t * 128];
-      __builtin_amdgcn_sched_barrier(0);
-      f32x16 s[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-        for (int n = NQ - 1; n >= 0; --n)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[c][t]), q[c][n], s[t], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
       // V of the first two key quarters while the products finish
       bf16x8 vf[2][S];
       const auto read_v = [&](int kc) {
@@ -421,7 +446,6 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       };
       read_v(0);
       read_v(1);
-      mfma_settle_before_join();
       __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
         uint64_t seen = below(pos - j0 + 1) & valid;
@@ -471,9 +495,11 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       };
       weights(0);
       __builtin_amdgcn_sched_barrier(0);
-      // the next quarter's weights are formed beside this one's products
+      // the next quarter's weights are formed beside this one's products, and
+      // the copies of tile i + 2 spread between them
 #pragma unroll
       for (int kc = 0; kc < 4; ++kc) {
+        if (kc < S) copy_block(src, after, kc);
         if (kc < 3) weights(kc + 1);
 #pragma unroll
         for (int d = 0; d < S; ++d)
@@ -495,6 +521,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     else if (few) run_tiles(Planes<2>());
     else run_tiles(Planes<1>());
     mfma_settle_before_join();
+    loads_done<0>();
     if (tid == 0) s_task = next_task;
     __syncthreads();  // the next item's first tile goes over a buffer that may still be read
     task = __builtin_amdgcn_readfirstlane(s_task);

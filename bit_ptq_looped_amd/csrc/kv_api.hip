@@ -36,6 +36,8 @@ int32_t check_shape(int pages, int slabs, int heads, int page_size, int head_dim
   if (st != LOOPQ_OK) return st;
   if (head_dim != 64 && head_dim != 96 && head_dim != 128) return LOOPQ_ERR_UNSUPPORTED;
   if ((int64_t)heads * head_dim > (1 << 20) || slabs > (1 << 16)) return LOOPQ_ERR_UNSUPPORTED;
+  // a page's bytes are a 32-bit factor in the kernels' addresses
+  if ((int64_t)slabs * 4 * heads * page_size * head_dim >= ((int64_t)1 << 31)) return LOOPQ_ERR_UNSUPPORTED;
   return LOOPQ_OK;
 }
 

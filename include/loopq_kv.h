@@ -26,8 +26,9 @@
  * page_size.
  *
  * Limits (LOOPQ_ERR_UNSUPPORTED outside them): head_dim 64, 96 or 128;
- * page_size a power of two in 8 .. 256; num_pages <= 2^22; rows <= 65536;
- * rows * max_pages < 2^31; heads_q a multiple of heads.
+ * page_size a power of two in 8 .. 256; a page below 2 GiB; num_pages <= 2^22;
+ * rows <= 8192; max_pages <= 2^22 and rows * max_pages < 2^31; heads_q a
+ * multiple of heads.
  *
  * The conventions of loopq.h hold: device pointers unless the name ends in
  * _host, work is enqueued on `stream` and the call returns, the caller owns
