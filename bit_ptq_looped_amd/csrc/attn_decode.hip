@@ -49,12 +49,155 @@ __device__ __forceinline__ int64_t decode_piece(int64_t total) {
   return n < 2 ? 2 : n;
 }
 
+// Tiles first .. last - 1 (at least one) of a query tile's keys, by one wave: O^T
+// in registers (lane: head lane % 16, columns 16 d + 4 (lane / 16) + r), the
+// reference m and l = the sum of the weights.  `tile` is the wave's own LDS.  K
+// goes from memory to the product's operand, V through LDS to be transposed; the
+// next tile's loads are issued before this one's weights are formed.
+template <int D, bool F32>
+__device__ __forceinline__ void decode_tiles(const AttnArgs& a, const AttnPlan& pl, int row, int kvh, int hq, bool has, int pos,
+                                             const Tiles& tl, int first, int last, u32x4* tile, f32x4 (&o)[D / 16],
+                                             float& m, float& l) {
+  constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
+  constexpr int C = D / 8;                  // chunks of a row
+  constexpr int NV = kDecodeKeys * C / 64;  // chunks of a tile per lane
+  const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+  const int32_t* table = a.table + (int64_t)row * a.width;
+  m = -INFINITY;
+  l = 0.0f;
+  bf16x8 q[D / 32][NQ];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+    load_query<NQ>(a, pl.qmul, row * a.ldq + (int64_t)hq * D + 32 * c + 8 * g, has, q[c]);
+
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
+
+  // lane x (mod 32) looks after key x of a tile: its page, or -1 if it is hidden
+  const auto page_of = [&](int i) {
+    const int j = (tl.at(i) << 5) + (lane & 31);
+    int page = -1;
+    if (sees(a, pos, j)) {
+      page = table[j >> a.page_shift];
+    }
+    return page;  // as it stands in the table: the load is not waited for here
+  };
+  const auto real = [&](int page) { return (uint32_t)page < (uint32_t)a.num_pages ? page : -1; };
+  u32x4 kr[2][D / 32], vr[NV];
+  const auto load_tile = [&](int i, int page) {
+    const int j0 = tl.at(i) << 5;
+    const int in_page = (1 << a.page_shift) - 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int key = 16 * t + n16, pg = __shfl(page, key, 64);
+      const uint16_t* p = a.pool + pg * a.page_stride + (((int64_t)kvh << a.page_shift) + ((j0 + key) & in_page)) * D + 8 * g;
+      if (pg >= 0)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) kr[t][c] = *reinterpret_cast<const u32x4*>(p + 32 * c);
+    }
+#pragma unroll
+    for (int x = 0; x < NV; ++x) {
+      const int at = lane + 64 * x, key = at / C, ch = at - key * C, pg = __shfl(page, key, 64);
+      const uint16_t* p = a.pool + a.plane + pg * a.page_stride +
+                          (((int64_t)kvh << a.page_shift) + ((j0 + key) & in_page)) * D + 8 * ch;
+      vr[x] = u32x4{0, 0, 0, 0};  // a hidden key's values count for nothing, whatever they hold
+      if (pg >= 0) vr[x] = *reinterpret_cast<const u32x4*>(p);
+    }
+  };
+
+  int page = real(page_of(first));
+  uint32_t seen = (uint32_t)__ballot(page >= 0);
+  load_tile(first, page);
+  page = first + 1 < last ? page_of(first + 1) : -1;
+  for (int i = first; i < last; ++i) {
+    // S^T: rows 4 g + r of key tile t, column n16
+    f32x4 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int n = NQ - 1; n >= 0; --n)
+          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kr[t][c]), q[c][n], s[t], 0, 0, 0);
+    }
+    // V to LDS, then the next tile's loads
+#pragma unroll
+    for (int x = 0; x < NV; ++x) {
+      const int at = lane + 64 * x, key = at / C, ch = at - key * C;
+      tile[chunk_at<5, true>(key, ch)] = vr[x];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    mfma_settle_before_join();
+    const uint32_t now = seen;
+    if (i + 1 < last) {
+      page = real(page);
+      seen = (uint32_t)__ballot(page >= 0);
+      load_tile(i + 1, page);
+      page = i + 2 < last ? page_of(i + 2) : -1;
+    }
+    if (now != 0xffffffffu) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (!((now >> (16 * t + 4 * g + r)) & 1)) s[t][r] = -INFINITY;
+    }
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    top *= pl.c;
+    if (__any(top > m)) {
+      const float mn = fmaxf(m, top);
+      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[d] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(fmaf(s[e >> 2][e & 3], pl.c, -ref));
+      l += p[e];
+    }
+    bf16x8 w[NP];
+    split_weights<NP>(p, w);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const int x = lane & 15, key = 4 * g + (x >> 2), ch = 2 * d + ((x & 3) >> 1);
+      const bf16x8 vt = join_halves(read_tr(tile, chunk_at<5, true>(key, ch), x & 1), read_tr(tile, chunk_at<5, true>(key + 16, ch), x & 1));
+#pragma unroll
+      for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, w[n], o[d], 0, 0, 0);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  mfma_settle_before_join();
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+}
+
+// one head's result from a lane's columns
+template <int D>
+__device__ __forceinline__ void store_columns(const AttnArgs& a, int64_t at, const f32x4 (&o)[D / 16], float l) {
+  const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) {
+    const f32x4 r = o[d] * f;
+    if (a.bf16)
+      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at + 16 * d) = u32x2{bf16x2_rne(r[0], r[1]), bf16x2_rne(r[2], r[3])};
+    else
+      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at + 16 * d) = r;
+  }
+}
+
 template <int D, bool F32>
 __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPlan pl) {
-  constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
-  constexpr int C = D / 8;               // chunks of a row
-  constexpr int NV = kDecodeKeys * C / 64;  // chunks of a tile per lane
-  __shared__ u32x4 s_v[4][kDecodeKeys * C];
+  __shared__ u32x4 s_v[4][kDecodeKeys * D / 8];
   extern __shared__ int64_t s_prefix[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n16 = lane & 15, g = lane >> 4;
@@ -78,135 +221,11 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
     const int head = gt * kDecodeRows + n16;  // in the group
     const bool has = head < a.group;
     const int hq = kvh * a.group + head;
-    const int32_t* table = a.table + (int64_t)row * a.width;
-
-    bf16x8 q[D / 32][NQ];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-      load_query<NQ>(a, pl.qmul, row * a.ldq + (int64_t)hq * D + 32 * c + 8 * g, has, q[c]);
-
     f32x4 o[D / 16];
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
-    float m = -INFINITY, l = 0.0f;
-
-    // lane x (mod 32) looks after key x of a tile: its page, or -1 if it is hidden
-    const auto page_of = [&](int i) {
-      const int j = (tl.at(i) << 5) + (lane & 31);
-      int page = -1;
-      if (sees(a, pos, j)) {
-        page = table[j >> a.page_shift];
-      }
-      return page;  // as it stands in the table: the load is not waited for here
-    };
-    const auto real = [&](int page) { return (uint32_t)page < (uint32_t)a.num_pages ? page : -1; };
-    u32x4 kr[2][D / 32], vr[NV];
-    const auto load_tile = [&](int i, int page) {
-      const int j0 = tl.at(i) << 5;
-      const int in_page = (1 << a.page_shift) - 1;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int key = 16 * t + n16, pg = __shfl(page, key, 64);
-        const uint16_t* p = a.pool + pg * a.page_stride + (((int64_t)kvh << a.page_shift) + ((j0 + key) & in_page)) * D + 8 * g;
-        if (pg >= 0)
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) kr[t][c] = *reinterpret_cast<const u32x4*>(p + 32 * c);
-      }
-#pragma unroll
-      for (int x = 0; x < NV; ++x) {
-        const int at = lane + 64 * x, key = at / C, ch = at - key * C, pg = __shfl(page, key, 64);
-        const uint16_t* p = a.pool + a.plane + pg * a.page_stride +
-                            (((int64_t)kvh << a.page_shift) + ((j0 + key) & in_page)) * D + 8 * ch;
-        vr[x] = u32x4{0, 0, 0, 0};  // a hidden key's values count for nothing, whatever they hold
-        if (pg >= 0) vr[x] = *reinterpret_cast<const u32x4*>(p);
-      }
-    };
-
-    int page = real(page_of(first));
-    uint32_t seen = (uint32_t)__ballot(page >= 0);
-    load_tile(first, page);
-    page = first + 1 < last ? page_of(first + 1) : -1;
-    for (int i = first; i < last; ++i) {
-      // S^T: rows 4 g + r of key tile t, column n16
-      f32x4 s[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-          for (int n = NQ - 1; n >= 0; --n)
-            s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kr[t][c]), q[c][n], s[t], 0, 0, 0);
-      }
-      // V to LDS, then the next tile's loads
-#pragma unroll
-      for (int x = 0; x < NV; ++x) {
-        const int at = lane + 64 * x, key = at / C, ch = at - key * C;
-        tile[chunk_at<5, true>(key, ch)] = vr[x];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      const uint32_t now = seen;
-      if (i + 1 < last) {
-        page = real(page);
-        seen = (uint32_t)__ballot(page >= 0);
-        load_tile(i + 1, page);
-        page = i + 2 < last ? page_of(i + 2) : -1;
-      }
-      if (now != 0xffffffffu) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (!((now >> (16 * t + 4 * g + r)) & 1)) s[t][r] = -INFINITY;
-      }
-      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      top *= pl.c;
-      if (__any(top > m)) {
-        const float mn = fmaxf(m, top);
-        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[d] *= f;
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      float p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(fmaf(s[e >> 2][e & 3], pl.c, -ref));
-        l += p[e];
-      }
-      bf16x8 w[NP];
-      split_weights<NP>(p, w);
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        const int x = lane & 15, key = 4 * g + (x >> 2), ch = 2 * d + ((x & 3) >> 1);
-        const bf16x8 vt = join_halves(read_tr(tile, chunk_at<5, true>(key, ch), x & 1), read_tr(tile, chunk_at<5, true>(key + 16, ch), x & 1));
-#pragma unroll
-        for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, w[n], o[d], 0, 0, 0);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
+    float m, l;
+    decode_tiles<D, F32>(a, pl, row, kvh, hq, has, pos, tl, first, last, tile, o, m, l);
     if (first == 0 && last == tl.n) {
-      const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-      if (has) {
-        const int64_t at = row * a.ldo + (int64_t)hq * D + 4 * g;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          const f32x4 r = o[d] * f;
-          if (a.bf16)
-            *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at + 16 * d) = u32x2{bf16x2_rne(r[0], r[1]), bf16x2_rne(r[2], r[3])};
-          else
-            *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at + 16 * d) = r;
-        }
-      }
+      if (has) store_columns<D>(a, row * a.ldo + (int64_t)hq * D + 4 * g, o, l);
     } else if (has) {
       const int second = first == 0 && u != idx * piece;
       const int64_t slot = (int64_t)idx * 2 + second;
@@ -230,6 +249,56 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
           if (a.bf16) reinterpret_cast<uint16_t*>(a.out)[r * a.ldo + d] = 0;
           else reinterpret_cast<float*>(a.out)[r * a.ldo + d] = 0.0f;
         }
+}
+
+// Short rows: a work-group per item, an eighth of its tiles a wave, joined in
+// LDS, so that there is no second launch and no trip through memory.
+constexpr int kShortWaves = 8;
+template <int D, bool F32>
+__global__ __launch_bounds__(64 * kShortWaves, 2) void decode_short_kernel(AttnArgs a, AttnPlan pl) {
+  __shared__ u32x4 s_v[kShortWaves][kDecodeKeys * D / 8];  // a wave's V tile, then its O: [16][D] floats, as many bytes
+  __shared__ float s_m[kShortWaves][kDecodeRows], s_l[kShortWaves][kDecodeRows];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, g = lane >> 4;
+  const int gts = (a.group + kDecodeRows - 1) / kDecodeRows, items = a.heads * gts;
+  const int row = blockIdx.x / items, item = blockIdx.x - row * items;
+  const int kvh = item / gts, gt = item - kvh * gts, head = gt * kDecodeRows + n16, hq = kvh * a.group + head;
+  const bool has = head < a.group;
+  const int pos = row_len(a, row) - 1;
+  const Tiles tl = visible_tiles(a, pos, pos, 5);
+  const int per = (tl.n + kShortWaves - 1) / kShortWaves, first = wave * per, last = min(first + per, tl.n);
+  float m = -INFINITY, l = 0.0f;
+  if (first < last) {
+    f32x4 o[D / 16];
+    decode_tiles<D, F32>(a, pl, row, kvh, hq, has, pos, tl, first, last, s_v[wave], o, m, l);
+    float* so = reinterpret_cast<float*>(s_v[wave]) + n16 * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4*>(so + 16 * d) = o[d];
+  }
+  if (g == 0) {
+    s_m[wave][n16] = m;
+    s_l[wave][n16] = l;
+  }
+  __syncthreads();
+  const int heads = min(kDecodeRows, a.group - gt * kDecodeRows);
+  for (int e = tid; e < heads * D; e += 64 * kShortWaves) {
+    const int r = e / D, d = e - r * D;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kShortWaves; ++w) top = fmaxf(top, s_m[w][r]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kShortWaves; ++w) {
+      if (w * per >= tl.n) break;  // the wave had no tile
+      const float f = __builtin_amdgcn_exp2f(s_m[w][r] - ref);
+      sum = fmaf(f, s_l[w][r], sum);
+      x = fmaf(f, reinterpret_cast<const float*>(s_v[w])[e], x);
+    }
+    x *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int64_t at = row * a.ldo + (int64_t)(kvh * a.group + gt * kDecodeRows) * D + e;
+    if (a.bf16) reinterpret_cast<uint16_t*>(a.out)[at] = (uint16_t)bf16x2_rne(x, 0.0f);
+    else reinterpret_cast<float*>(a.out)[at] = x;
+  }
 }
 
 // Joins split items: one work-group per (item, head), its four waves a quarter
@@ -264,6 +333,17 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a, AttnPlan p
 
 template <int D, bool F32>
 hipError_t launch(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+  // By what the table has room for, since lengths are not known here.  D = 128,
+  // bf16, every row full, us (short, cut): one row of 16 heads: 512 keys 10.8,
+  // 15.2; 1024 keys 16.1, 15.8; 4096 keys 44, 17.  8 rows of 16 heads: 512 keys
+  // 12.2, 17.4; 2048 keys 28, 35; 8192 keys 125, 112.  64 rows of 20 heads: 256
+  // keys 45, 41; 2048 keys 239, 255.
+  const int items = a.heads * ((a.group + kDecodeRows - 1) / kDecodeRows);
+  const int64_t room = (int64_t)a.width << a.page_shift;
+  if (room <= 512 || (room <= 2048 && (int64_t)a.rows * items >= 128)) {
+    decode_short_kernel<D, F32><<<a.rows * items, 64 * kShortWaves, 0, s>>>(a, pl);
+    return hipGetLastError();
+  }
   const int lds = (a.rows + 1) * 8;
   const hipError_t e = prepare_launch(reinterpret_cast<const void*>(decode_attn_kernel<D, F32>), lds, 256);
   if (e != hipSuccess) return e;

@@ -15,6 +15,12 @@ namespace loopq {
 namespace {
 
 constexpr int kScan = 1024;  // threads of the one-work-group kernels
+// Tables and counts of up to this many entries are handled by one work-group,
+// which saves a launch (about 3 us of host and 2 us of device time each).
+constexpr int kOneGroup = 16384;
+// Work-groups of a copy of pages, at most: 2048 leave the memory's queues short
+// (evict of 0.8 GB 354 us, with 16384 331 us).
+constexpr int kCopyGroups = 16384;
 
 __device__ __forceinline__ int clamped_len(const KvTable& t, int row, int shift) {
   const int64_t cap = (int64_t)t.width << shift;
@@ -200,14 +206,14 @@ __device__ __forceinline__ void copy_chunk(const char* src, char* dst, int64_t a
   const u32x4* s = reinterpret_cast<const u32x4*>(src + at);
   u32x4* d = reinterpret_cast<u32x4*>(dst + at);
   const int n = (int)(min((int64_t)kChunk, bytes - at) / 16);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x & 255;
   u32x4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (tid + 256 * i < n) v[i] = __builtin_nontemporal_load(s + tid + 256 * i);
+    if (tid + 256 * i < n) v[i] = s[tid + 256 * i];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (tid + 256 * i < n) __builtin_nontemporal_store(v[i], d + tid + 256 * i);
+    if (tid + 256 * i < n) d[tid + 256 * i] = v[i];
 }
 
 __global__ __launch_bounds__(256) void copy_pages_kernel(const char* src_pool, int src_pages, const int32_t* src,
@@ -250,63 +256,126 @@ __global__ __launch_bounds__(256) void fork_gather_kernel(KvTable in, KvTable ou
   fork_gather(in, out, parent, bits, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
-// One work-group: children of each row, who keeps the partial last page, the
-// pages of the copies.
-template <bool FUSED>
-__global__ __launch_bounds__(kScan) void fork_plan_kernel(KvTable in, KvTable out, int shift, const int32_t* parent,
-                                                          int32_t* info, KvScratch w) {
-  __shared__ int s_first[kKvMaxRows], s_children[kKvMaxRows];
+// By one work-group of 1024: children of each row of in (and the first of them)
+// into LDS, the pages that are copied into src and their places into dst, by
+// rank; their number, or -1 if the free pages do not suffice (*need says how
+// many it would take).  at_of(i, k, page) is told that row i's last page is copy
+// k.
+template <class F>
+__device__ __forceinline__ int fork_plan(const KvTable& in, int out_rows, int shift, const int32_t* parent,
+                                         const uint64_t* bits, int* first, int* children, int32_t* src, int32_t* dst,
+                                         int* need, F at_of) {
   const int tid = threadIdx.x;
-  if (FUSED) fork_gather(in, out, parent, w.bits, tid, kScan);
   for (int r = tid; r < in.rows; r += kScan) {
-    s_first[r] = 0x7fffffff;
-    s_children[r] = 0;
+    first[r] = 0x7fffffff;
+    children[r] = 0;
   }
   __syncthreads();
-  for (int i = tid; i < out.rows; i += kScan) {
+  for (int i = tid; i < out_rows; i += kScan) {
     const int p = parent_of(parent, i, in.rows);
     if (p >= 0) {
-      atomicMin(&s_first[p], i);
-      atomicAdd(&s_children[p], 1);
+      atomicMin(&first[p], i);
+      atomicAdd(&children[p], 1);
     }
   }
   __syncthreads();
-  for (int r = tid; r < in.rows; r += kScan) w.row_b[r] = s_children[r];
   int total = 0;
-  for (int i0 = 0; i0 < out.rows; i0 += kScan) {
+  for (int i0 = 0; i0 < out_rows; i0 += kScan) {
     const int i = i0 + tid;
     int page = -1;
-    if (i < out.rows) {
+    if (i < out_rows) {
       const int p = parent_of(parent, i, in.rows);
       const int len = p < 0 ? 0 : clamped_len(in, p, shift);
       if (len & ((1 << shift) - 1)) {
         page = in.table[(int64_t)p * in.width + (len >> shift)];
-        if (page < 0 || page >= in.pages || (s_first[p] == i && in.refs[page] == 1)) page = -1;
+        if (page < 0 || page >= in.pages || (first[p] == i && in.refs[page] == 1)) page = -1;
       }
     }
     int all;
     const int before = block_exclusive(page >= 0 ? 1 : 0, &all);
-    if (i < out.rows) w.row_a[i] = page >= 0 ? total + before : -1;
-    if (page >= 0) w.src[total + before] = page;
+    if (i < out_rows) at_of(i, page >= 0 ? total + before : -1);
+    if (page >= 0) src[total + before] = page;
     total += all;
   }
-  const int nfree = list_bits(w.bits, (in.pages + 63) >> 6, w.list, total);
+  *need = total;
+  const int nfree = list_bits(bits, (in.pages + 63) >> 6, dst, total);
   __syncthreads();
-  const bool fail = total > nfree;
+  return total > nfree ? -1 : total;
+}
+
+__global__ __launch_bounds__(kScan) void fork_plan_kernel(KvTable in, KvTable out, int shift, const int32_t* parent,
+                                                          int32_t* info, KvScratch w) {
+  __shared__ int s_first[kKvMaxRows], s_children[kKvMaxRows];
+  const int tid = threadIdx.x;
+  int need;
+  const int n = fork_plan(in, out.rows, shift, parent, w.bits, s_first, s_children, w.src, w.list, &need,
+                          [&](int i, int k) { w.row_a[i] = k; });
+  for (int r = tid; r < in.rows; r += kScan) w.row_b[r] = s_children[r];
   if (tid == 0) {
-    info[0] = fail ? LOOPQ_KV_NO_PAGES : LOOPQ_KV_DONE;
-    info[1] = total;
-    w.head[0] = fail ? 0 : total;
-    w.head[1] = fail;
+    info[0] = n < 0 ? LOOPQ_KV_NO_PAGES : LOOPQ_KV_DONE;
+    info[1] = need;
+    w.head[0] = max(n, 0);
+    w.head[1] = n < 0;
   }
-  if (fail) return;
+  if (n < 0) return;
   for (int i = tid; i < out.rows; i += kScan) {
     const int k = w.row_a[i];
     if (k < 0) continue;
     const int p = parent_of(parent, i, in.rows);
-    const int page = w.list[k];
-    w.dst[k] = page;
-    out.table[(int64_t)i * out.width + (clamped_len(in, p, shift) >> shift)] = page;
+    w.dst[k] = w.list[k];
+    out.table[(int64_t)i * out.width + (clamped_len(in, p, shift) >> shift)] = w.list[k];
+  }
+}
+
+// The whole fork in one launch, for small tables and pools: every work-group
+// plans it for itself (in LDS, from the same inputs), then takes its share of
+// the rows and of the contents; the first one has the reference counts.
+constexpr int kForkRows = 1024, kForkPages = 8192;
+__global__ __launch_bounds__(kScan) void fork_one_kernel(KvTable in, KvTable out, int shift, const int32_t* parent,
+                                                         int32_t* info, char* pool, int64_t page_bytes) {
+  __shared__ uint64_t s_bits[kForkPages / 64];
+  __shared__ int s_first[kForkRows], s_children[kForkRows], s_rank[kForkRows], s_src[kForkRows], s_dst[kForkRows];
+  __shared__ int s_refs[kForkPages];
+  const int tid = threadIdx.x;
+  page_bits(in.refs, in.pages, s_bits, true, tid, kScan);
+  int need;
+  const int n = fork_plan(in, out.rows, shift, parent, s_bits, s_first, s_children, s_src, s_dst, &need,
+                          [&](int i, int k) { s_rank[i] = k; });
+  __syncthreads();
+  for (int i = blockIdx.x; i < out.rows; i += gridDim.x) {
+    const int p = parent_of(parent, i, in.rows), k = s_rank[i];
+    const int copied = n >= 0 && k >= 0 ? clamped_len(in, p, shift) >> shift : -1;
+    for (int c = tid; c < out.width; c += kScan)
+      out.table[(int64_t)i * out.width + c] = p < 0 || n < 0 ? -1 : c == copied ? s_dst[k] : in.table[(int64_t)p * in.width + c];
+    if (tid == 0) out.lens[i] = p < 0 || n < 0 ? 0 : in.lens[p];
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+    if (tid == 0) {
+      info[0] = n < 0 ? LOOPQ_KV_NO_PAGES : LOOPQ_KV_DONE;
+      info[1] = need;
+    }
+    for (int p = tid; p < in.pages; p += kScan) s_refs[p] = in.refs[p];
+    __syncthreads();
+    if (n >= 0) {
+      for (int i = tid; i < in.rows * in.width; i += kScan) {
+        const int more = s_children[i / in.width] - 1;
+        const int page = in.table[i];
+        if (more != 0 && page >= 0 && page < in.pages) atomicAdd(&s_refs[page], more);
+      }
+      for (int m = tid; m < n; m += kScan) {
+        atomicAdd(&s_refs[s_src[m]], -1);
+        atomicAdd(&s_refs[s_dst[m]], 1);
+      }
+    }
+    __syncthreads();
+    for (int p = tid; p < in.pages; p += kScan) out.refs[p] = s_refs[p];
+  }
+  // four chunks of 16 KiB at a time
+  const int64_t chunks = (page_bytes + 4 * kChunk - 1) / (4 * kChunk), all = chunks * n;
+  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+    const int m = (int)(i / chunks);
+    const int64_t at = (i - m * chunks) * 4 * kChunk + (tid >> 8) * kChunk;
+    if (at < page_bytes) copy_chunk(pool + s_src[m] * page_bytes, pool + s_dst[m] * page_bytes, at, page_bytes);
   }
 }
 
@@ -344,18 +413,30 @@ __global__ __launch_bounds__(256) void copy_refs_kernel(const int32_t* in, int32
   if (i < n) out[i] = in[i];
 }
 
-__global__ __launch_bounds__(256) void trim_kernel(KvTable in, KvTable out, int shift, int window, int sinks) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)in.rows * in.width) return;
-  const int row = (int)(i / in.width);
-  const int64_t k = i - (int64_t)row * in.width;
-  int page = in.table[i];
-  if (((k + 1) << shift) <= (int64_t)clamped_len(in, row, shift) - window + 1 && (k << shift) >= sinks) {
-    if (page >= 0 && page < in.pages) atomicAdd(&out.refs[page], -1);
-    page = -1;
+__device__ __forceinline__ void trim_entries(const KvTable& in, const KvTable& out, int shift, int window, int sinks,
+                                             int64_t first, int64_t step) {
+  for (int64_t i = first; i < (int64_t)in.rows * in.width; i += step) {
+    const int row = (int)(i / in.width);
+    const int64_t k = i - (int64_t)row * in.width;
+    int page = in.table[i];
+    if (((k + 1) << shift) <= (int64_t)clamped_len(in, row, shift) - window + 1 && (k << shift) >= sinks) {
+      if (page >= 0 && page < in.pages) atomicAdd(&out.refs[page], -1);
+      page = -1;
+    }
+    out.table[i] = page;
+    if (k == 0) out.lens[row] = in.lens[row];
   }
-  out.table[i] = page;
-  if (k == 0) out.lens[row] = in.lens[row];
+}
+
+__global__ __launch_bounds__(256) void trim_kernel(KvTable in, KvTable out, int shift, int window, int sinks) {
+  trim_entries(in, out, shift, window, sinks, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+__global__ __launch_bounds__(kScan) void trim_one_kernel(KvTable in, KvTable out, int shift, int window, int sinks) {
+  if (in.refs != out.refs)
+    for (int p = threadIdx.x; p < in.pages; p += kScan) out.refs[p] = in.refs[p];
+  __syncthreads();
+  trim_entries(in, out, shift, window, sinks, threadIdx.x, kScan);
 }
 
 // ------------------------------------------------------------------ compact
@@ -365,7 +446,12 @@ __global__ __launch_bounds__(256) void used_bits_kernel(const int32_t* refs, int
 }
 
 // used pages before each word; their number L and how many lie at L or above
-__global__ __launch_bounds__(kScan) void compact_scan_kernel(KvScratch w, int words, int32_t* info) {
+__global__ __launch_bounds__(kScan) void compact_scan_kernel(KvScratch w, int words, int32_t* info, const int32_t* refs,
+                                                             int pages) {
+  if (refs) {  // the bits, too
+    page_bits(refs, pages, w.bits, false, threadIdx.x, kScan);
+    __syncthreads();
+  }
   int base = 0;
   for (int w0 = 0; w0 < words; w0 += kScan) {
     const int i = w0 + threadIdx.x;
@@ -441,11 +527,13 @@ __global__ __launch_bounds__(256) void compact_apply_kernel(KvTable in, KvTable 
   }
   if (in.lens != out.lens)
     for (int64_t i = first; i < in.rows; i += step) out.lens[i] = in.lens[i];
+  // each work-group moves a run of chunks: the search for a page's places is paid once a page
   const int64_t chunks = (page_bytes + kChunk - 1) / kChunk, n = chunks * w.head[0];
+  const int64_t per = (n + gridDim.x - 1) / gridDim.x, end = min((blockIdx.x + 1) * per, n);
   int last = -1;
   const char* from = nullptr;
   char* to = nullptr;
-  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+  for (int64_t i = blockIdx.x * per; i < end; ++i) {
     const int m = (int)(i / chunks);
     if (m != last) {
       const int p = u.nth_used(u.below + m);
@@ -497,8 +585,12 @@ hipError_t launch_kv_reserve(KvTable in, KvTable out, int page_size, const int32
                              hipStream_t s) {
   const int shift = shift_of(page_size);
   const int64_t n = (int64_t)in.pages + (int64_t)in.rows * in.width;
-  reserve_copy_kernel<<<blocks_for(n, 1024), 256, 0, s>>>(in, out, w.bits);
-  reserve_kernel<false><<<1, kScan, 0, s>>>(in, out, shift, grow, info, w);
+  if (n <= kOneGroup) {
+    reserve_kernel<true><<<1, kScan, 0, s>>>(in, out, shift, grow, info, w);
+  } else {
+    reserve_copy_kernel<<<blocks_for(n, 1024), 256, 0, s>>>(in, out, w.bits);
+    reserve_kernel<false><<<1, kScan, 0, s>>>(in, out, shift, grow, info, w);
+  }
   return hipGetLastError();
 }
 
@@ -512,28 +604,40 @@ hipError_t launch_kv_fork(KvTable in, KvTable out, int page_size, void* pool, in
                           int32_t* info, KvScratch w, hipStream_t s) {
   const int shift = shift_of(page_size);
   const int64_t n = (int64_t)in.pages + (int64_t)out.rows * out.width;
+  if (in.pages <= kForkPages && max(in.rows, out.rows) <= kForkRows && (int64_t)in.rows * in.width <= kOneGroup) {
+    const int64_t most = max((int64_t)out.rows * ((page_bytes + 4 * kChunk - 1) / (4 * kChunk)), (int64_t)1);
+    fork_one_kernel<<<(int)min(most, (int64_t)256), kScan, 0, s>>>(in, out, shift, parent, info,
+                                                                  reinterpret_cast<char*>(pool), page_bytes);
+    return hipGetLastError();
+  }
   fork_gather_kernel<<<blocks_for(n, 1024), 256, 0, s>>>(in, out, parent, w.bits);
-  fork_plan_kernel<false><<<1, kScan, 0, s>>>(in, out, shift, parent, info, w);
+  fork_plan_kernel<<<1, kScan, 0, s>>>(in, out, shift, parent, info, w);
   const int64_t items = max((int64_t)in.rows * in.width, (int64_t)out.rows * out.width);
   const int64_t chunks = out.rows * ((page_bytes + kChunk - 1) / kChunk);  // at most
-  fork_apply_kernel<<<blocks_for(max(items, chunks * 256), 2048), 256, 0, s>>>(in, out, reinterpret_cast<char*>(pool),
+  fork_apply_kernel<<<blocks_for(max(items, chunks * 256), kCopyGroups), 256, 0, s>>>(in, out, reinterpret_cast<char*>(pool),
                                                                              page_bytes, w);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_trim(KvTable in, KvTable out, int page_size, int window, int sinks, hipStream_t s) {
-  if (in.refs != out.refs) copy_refs_kernel<<<(in.pages + 255) / 256, 256, 0, s>>>(in.refs, out.refs, in.pages);
   const int64_t n = (int64_t)in.rows * in.width;
-  trim_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(in, out, shift_of(page_size), window, sinks);
+  const int shift = shift_of(page_size);
+  if (in.pages + n <= kOneGroup) {
+    trim_one_kernel<<<1, kScan, 0, s>>>(in, out, shift, window, sinks);
+  } else {
+    if (in.refs != out.refs) copy_refs_kernel<<<(in.pages + 255) / 256, 256, 0, s>>>(in.refs, out.refs, in.pages);
+    trim_kernel<<<blocks_for(n, 2048), 256, 0, s>>>(in, out, shift, window, sinks);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_kv_compact(KvTable in, KvTable out, void* pool, int64_t page_bytes, int32_t* page_map, int32_t* info,
                              KvScratch w, hipStream_t s) {
-  used_bits_kernel<<<blocks_for(in.pages, 1024), 256, 0, s>>>(in.refs, in.pages, w.bits);
-  compact_scan_kernel<<<1, kScan, 0, s>>>(w, (in.pages + 63) / 64, info);
+  const bool one = in.pages <= kOneGroup;
+  if (!one) used_bits_kernel<<<blocks_for(in.pages, 1024), 256, 0, s>>>(in.refs, in.pages, w.bits);
+  compact_scan_kernel<<<1, kScan, 0, s>>>(w, (in.pages + 63) / 64, info, one ? in.refs : nullptr, in.pages);
   const int64_t chunks = in.pages * ((page_bytes + kChunk - 1) / kChunk);  // at most
-  compact_apply_kernel<<<blocks_for(max((int64_t)in.rows * in.width, chunks * 256), 2048), 256, 0, s>>>(
+  compact_apply_kernel<<<blocks_for(max((int64_t)in.rows * in.width, chunks * 256), kCopyGroups), 256, 0, s>>>(
       in, out, reinterpret_cast<char*>(pool), page_bytes, page_map, w);
   return hipGetLastError();
 }
@@ -541,7 +645,7 @@ hipError_t launch_kv_compact(KvTable in, KvTable out, void* pool, int64_t page_b
 hipError_t launch_kv_copy(const void* src_pool, int src_pages, const int32_t* src, void* dst_pool, int dst_pages,
                           const int32_t* dst, int count, int64_t page_bytes, hipStream_t s) {
   const int64_t chunks = count * ((page_bytes + kChunk - 1) / kChunk);
-  copy_pages_kernel<<<blocks_for(chunks * 256, 2048), 256, 0, s>>>(
+  copy_pages_kernel<<<blocks_for(chunks * 256, kCopyGroups), 256, 0, s>>>(
       reinterpret_cast<const char*>(src_pool), src_pages, src, reinterpret_cast<char*>(dst_pool), dst_pages, dst, count,
       page_bytes);
   return hipGetLastError();

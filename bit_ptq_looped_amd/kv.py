@@ -35,6 +35,7 @@ class _Table(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("rows", "max_pages", "num_pages")]
 
 
+_ref = ctypes.byref
 _P, _I, _F, _Z, _L = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
 _ZP, _PP, _TP = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(_Pool), ctypes.POINTER(_Table)
 # every entry point of include/loopq_kv.h with its ctypes signature
@@ -70,34 +71,46 @@ def load():
 
 def _pool(t) -> _Pool:
     """pool tensor bf16 [num_pages][slabs][2][heads][page_size][head_dim]"""
-    torch = loopq._torch_mod()
-    if t.dtype != torch.bfloat16 or t.dim() != 6 or t.shape[2] != 2 or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) != 6 or shape[2] != 2 or t.dtype is not _types().bfloat16 or not t.is_contiguous():
         raise ValueError("a pool is a contiguous bfloat16 tensor [pages][slabs][2][heads][page_size][head_dim]")
-    P, S, _, H, n, D = t.shape
+    P, S, _, H, n, D = shape
     return _Pool(_ptr(t), P, S, H, n, D)
 
 
-def _ints(t, what: str, n=None):
-    torch = loopq._torch_mod()
-    if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() < n):
-        raise ValueError(f"{what}: a contiguous int32 tensor" + (f" of at least {n} values" if n is not None else ""))
+_torch = None
+
+
+def _types():
+    global _torch
+    if _torch is None:
+        _torch = loopq._torch_mod()
+    return _torch
+
+
+def _ints(t, what: str, n: int = 0) -> int:
+    if t.dtype is not _types().int32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} values")
     return _ptr(t)
 
 
 def _table(t: KVTable) -> _Table:
-    if t.table.dim() != 2 or t.lens.numel() != t.table.shape[0]:
+    table, lens, refs = t
+    shape = table.shape
+    if len(shape) != 2 or lens.numel() != shape[0]:
         raise ValueError("a table is [rows][max_pages] with one length per row")
-    return _Table(_ints(t.table, "table"), _ints(t.lens, "lens"), _ints(t.refs, "refs"), t.table.shape[0],
-                  t.table.shape[1], t.refs.numel())
+    return _Table(_ints(table, "table"), _ints(lens, "lens"), _ints(refs, "refs"), shape[0], shape[1], refs.numel())
 
 
-def _rows3(x, heads, dim, what: str):
+def _rows3(x, heads, dim: int, what: str):
     """Pointer and row distance of [tokens][heads][dim] with dense heads."""
-    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{what}: expected [tokens][{heads if heads is not None else 'heads'}][{dim}], got {tuple(x.shape)}")
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != dim)):
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{what}: expected [tokens][{heads if heads is not None else 'heads'}][{dim}], got {tuple(shape)}")
+    row, head, one = x.stride()
+    if (one != 1 or (head != dim and shape[1] > 1)) and x.numel():
         raise ValueError(f"{what}: heads and elements of a token must be dense")
-    return _ptr(x), (x.stride(0) if x.shape[0] > 1 else x.shape[1] * dim)
+    return _ptr(x), (row if shape[0] > 1 else shape[1] * dim)
 
 
 def _ws(workspace):
@@ -108,20 +121,20 @@ def _ws(workspace):
 
 def loopq_kv_pool_bytes(num_pages: int, slabs: int, heads: int, page_size: int, head_dim: int) -> int:
     b = ctypes.c_size_t()
-    _check(load().loopq_kv_pool_bytes(num_pages, slabs, heads, page_size, head_dim, ctypes.byref(b)),
+    _check(load().loopq_kv_pool_bytes(num_pages, slabs, heads, page_size, head_dim, _ref(b)),
            "loopq_kv_pool_bytes")
     return b.value
 
 
 def loopq_kv_workspace_bytes(rows: int, num_pages: int) -> int:
     b = ctypes.c_size_t()
-    _check(load().loopq_kv_workspace_bytes(rows, num_pages, ctypes.byref(b)), "loopq_kv_workspace_bytes")
+    _check(load().loopq_kv_workspace_bytes(rows, num_pages, _ref(b)), "loopq_kv_workspace_bytes")
     return b.value
 
 
 def loopq_attn_workspace_bytes(queries: int, heads_q: int, rows: int, head_dim: int) -> int:
     b = ctypes.c_size_t()
-    _check(load().loopq_attn_workspace_bytes(queries, heads_q, rows, head_dim, ctypes.byref(b)),
+    _check(load().loopq_attn_workspace_bytes(queries, heads_q, rows, head_dim, _ref(b)),
            "loopq_attn_workspace_bytes")
     return b.value
 
@@ -130,8 +143,8 @@ def loopq_attn_workspace_bytes(queries: int, heads_q: int, rows: int, head_dim: 
 
 def loopq_kv_reserve(table: KVTable, page_size: int, grow, out: KVTable, info, workspace, stream=None):
     """Room for grow[b] more tokens in each row; out may be table itself."""
-    _check(load().loopq_kv_reserve(ctypes.byref(_table(table)), page_size, _ints(grow, "grow", table.lens.numel()),
-                                   ctypes.byref(_table(out)), _ints(info, "info", 2), *_ws(workspace),
+    _check(load().loopq_kv_reserve(_ref(_table(table)), page_size, _ints(grow, "grow", table.lens.numel()),
+                                   _ref(_table(out)), _ints(info, "info", 2), *_ws(workspace),
                                    _stream(stream)), "loopq_kv_reserve")
 
 
@@ -142,27 +155,27 @@ def loopq_kv_write(pool, slab: int, table: KVTable, cu, k, v, stream=None):
     vp, ldv = _rows3(v, p.heads, p.head_dim, "v")
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must have one type and shape")
-    _check(load().loopq_kv_write(ctypes.byref(p), slab, ctypes.byref(_table(table)),
+    _check(load().loopq_kv_write(_ref(p), slab, _ref(_table(table)),
                                  _ints(cu, "cu", table.lens.numel() + 1), kp, ldk, vp, ldv, _dtype_code(k),
                                  k.shape[0], _stream(stream)), "loopq_kv_write")
 
 
 def loopq_kv_fork(pool, table: KVTable, parent, out: KVTable, info, workspace, stream=None):
     """Row i of out takes the tokens of row parent[i] of table."""
-    _check(load().loopq_kv_fork(ctypes.byref(_pool(pool)), ctypes.byref(_table(table)),
-                                _ints(parent, "parent", out.lens.numel()), ctypes.byref(_table(out)),
+    _check(load().loopq_kv_fork(_ref(_pool(pool)), _ref(_table(table)),
+                                _ints(parent, "parent", out.lens.numel()), _ref(_table(out)),
                                 _ints(info, "info", 2), *_ws(workspace), _stream(stream)), "loopq_kv_fork")
 
 
 def loopq_kv_trim(table: KVTable, page_size: int, window: int, sinks: int, out: KVTable, stream=None):
     """Drop the pages that a sliding window has left behind; out may be table."""
-    _check(load().loopq_kv_trim(ctypes.byref(_table(table)), page_size, window, sinks, ctypes.byref(_table(out)),
+    _check(load().loopq_kv_trim(_ref(_table(table)), page_size, window, sinks, _ref(_table(out)),
                                 _stream(stream)), "loopq_kv_trim")
 
 
 def loopq_kv_compact(pool, table: KVTable, out: KVTable, page_map, info, workspace, stream=None):
     """Move the used pages to the front of the pool; out may be table itself."""
-    _check(load().loopq_kv_compact(ctypes.byref(_pool(pool)), ctypes.byref(_table(table)), ctypes.byref(_table(out)),
+    _check(load().loopq_kv_compact(_ref(_pool(pool)), _ref(_table(table)), _ref(_table(out)),
                                    _ints(page_map, "page_map", table.refs.numel()), _ints(info, "info", 2),
                                    *_ws(workspace), _stream(stream)), "loopq_kv_compact")
 
@@ -171,7 +184,7 @@ def loopq_kv_copy_pages(src_pool, src, dst_pool, dst, stream=None):
     """Page dst[i] of dst_pool = page src[i] of src_pool."""
     if src.numel() != dst.numel():
         raise ValueError("src and dst must have one length")
-    _check(load().loopq_kv_copy_pages(ctypes.byref(_pool(src_pool)), _ints(src, "src"), ctypes.byref(_pool(dst_pool)),
+    _check(load().loopq_kv_copy_pages(_ref(_pool(src_pool)), _ints(src, "src"), _ref(_pool(dst_pool)),
                                       _ints(dst, "dst"), src.numel(), _stream(stream)), "loopq_kv_copy_pages")
 
 
@@ -189,7 +202,7 @@ def loopq_attn_decode(pool, slab: int, table: KVTable, q, out, workspace, scale:
     _out_like(q, out)
     if q.shape[0] != table.lens.numel():
         raise ValueError("one query per row")
-    _check(load().loopq_attn_decode(ctypes.byref(p), slab, ctypes.byref(_table(table)), qp, ldq, _dtype_code(q),
+    _check(load().loopq_attn_decode(_ref(p), slab, _ref(_table(table)), qp, ldq, _dtype_code(q),
                                     q.shape[1], scale, window, sinks, op, ldo, *_ws(workspace), _stream(stream)),
            "loopq_attn_decode")
 
@@ -201,7 +214,7 @@ def loopq_attn_prefill(pool, slab: int, table: KVTable, cu, q, out, workspace, s
     qp, ldq = _rows3(q, None, p.head_dim, "q")
     op, ldo = _rows3(out, None, p.head_dim, "out")
     _out_like(q, out)
-    _check(load().loopq_attn_prefill(ctypes.byref(p), slab, ctypes.byref(_table(table)),
+    _check(load().loopq_attn_prefill(_ref(p), slab, _ref(_table(table)),
                                      _ints(cu, "cu", table.lens.numel() + 1), qp, ldq, _dtype_code(q), q.shape[0],
                                      q.shape[1], scale, window, sinks, op, ldo, *_ws(workspace), _stream(stream)),
            "loopq_attn_prefill")
