@@ -165,15 +165,16 @@ __device__ __forceinline__ PrefillItem prefill_item(const AttnArgs& a, const Att
   return it;
 }
 
-// 16 bytes per lane from src + OFF (bytes, per lane) to LDS at byte dst + 16
-// lane (dst a scalar), without passing the registers.  The compiler does not see
+// 16 bytes per lane from src + OFF (bytes, per lane) to LDS at byte dst + DST +
+// 16 lane (dst a scalar), without passing the registers.  The compiler does not see
 // the write: a reader waits for loads_done() and the barrier after it.  The
 // offset counts for the target, too; one wait state lies between the write of
 // m0 and its use.
-template <int OFF>
+template <int OFF, int DST>
 __device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(dst - OFF), "v"(src), "n"(OFF)
-               : "memory", "m0");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(dst), "v"(src), "n"(OFF),
+               "n"(DST - OFF)
+               : "memory", "m0", "scc");
 }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
@@ -188,6 +189,31 @@ __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
 }
 
+// A barrier in two halves, so that waves may be up to a tile apart: while some
+// form weights, others multiply.  A wave arrives once what it promises is done
+// (LDS operations of a wave keep their order); every wave arrives the same
+// number of times, and what it waits for lies before what others wait for.
+__device__ __forceinline__ void arrive(int* count) {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  if ((threadIdx.x & 63) == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ int look(int* count) {
+  return __hip_atomic_load(count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+// `seen` is an earlier look, taken where its latency is hidden: counts only grow
+__device__ __forceinline__ void wait_for(int* count, int n, int seen) {
+  __builtin_amdgcn_sched_barrier(0);
+  while (__builtin_amdgcn_readfirstlane(seen) < n) {
+    __builtin_amdgcn_s_sleep(1);
+    seen = look(count);
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // whether every key of a tile of 64 has a page
 __device__ __forceinline__ bool tile_has_pages(const AttnArgs& a, const int32_t* table, int tile) {
   bool ok = true;
@@ -197,8 +223,8 @@ __device__ __forceinline__ bool tile_has_pages(const AttnArgs& a, const int32_t*
 }
 
 // A work-group takes a task after another: W waves of 32 rows each over tiles of
-// 64 keys, K and V of the next two tiles on their way to a ring of three buffers
-// in LDS while one is multiplied.  Keys that no query of the item sees are read
+// 64 keys, K and V of the next three tiles on their way to a ring of four
+// buffers in LDS while one is multiplied.  Keys that no query of the item sees are read
 // from a line of zeros.  fp32 queries hold three planes in registers and take
 // half the rows.
 template <int D, bool F32, int W>
@@ -208,11 +234,13 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   constexpr int C = D / 8, S = D / 32;  // chunks and blocks of a row
   constexpr int kTile = kPrefillKeys * C;
   constexpr int kCopies = 8 * S / W;  // of a wave for one tile
-  __shared__ u32x4 s_k[3 * kTile], s_v[3 * kTile];
-  __shared__ __attribute__((aligned(8))) uint16_t s_valid[3][4];  // keys of a tile that some query sees, 16 a wave
+  constexpr int R = 4;  // buffers of the ring: copies run three tiles ahead
+  __shared__ u32x4 s_k[R * kTile], s_v[R * kTile];
+  __shared__ __attribute__((aligned(8))) uint16_t s_valid[R][4];  // keys of a tile that some query sees, 16 a wave
   __shared__ int s_pages[512];  // of 64 tiles' groups of eight keys
   __shared__ int s_task;
-  __shared__ int s_bad;  // a tile that some query sees in part had a value that is not finite
+  __shared__ int s_odd;     // some result is not finite
+  __shared__ int s_here, s_left;  // waves whose copies of a tile have landed; that have left a tile; counted over the task
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n32 = lane & 31, h = lane >> 5;
   const int in_page = (1 << a.page_shift) - 1;
@@ -233,16 +261,13 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   const uint32_t my_off = (my_key & in_page) * (2 * D) + 16 * ((lane & 3) ^ (lane >> 4)), page_bytes = (uint32_t)(2 * a.page_stride);
   const uint32_t to_k = lds_offset(s_k) + (wave0 & 3) * 1024, to_v = lds_offset(s_v) + (wave0 & 3) * 1024;
   // chunks this lane multiplies
-  int k_at[D / 16], v_at[S][2];
+  int k_at[2], v_at[2];  // in the first block; the others follow every 256 chunks
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) k_at[c] = chunk_at<6, false>(n32, 2 * c + h);
-  {
+  for (int c = 0; c < 2; ++c) k_at[c] = chunk_at<6, false>(n32, 2 * c + h);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
     const int x = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int d = 0; d < S; ++d)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        v_at[d][e] = chunk_at<6, false>(4 * h + 8 * e + (x >> 2), 4 * d + 2 * (g & 1) + ((x & 3) >> 1)) * 2 + (x & 1);
+    v_at[e] = chunk_at<6, false>(4 * h + 8 * e + (x >> 2), 2 * (g & 1) + ((x & 3) >> 1));
   }
 
   for (;;) {
@@ -271,7 +296,6 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       task = __builtin_amdgcn_readfirstlane(s_task);
       if (task < 0) return;
     }
-    if (tid == 0) s_bad = 0;
     const PrefillItem it = prefill_item<ROWS>(a, pl, task);
     const int first = it.from, last = it.to;
     // the eighth's next task, while this one runs
@@ -299,11 +323,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       load_query<NQ>(a, pl.qmul, (int64_t)(it.first + qi) * a.ldq + (int64_t)hq * D + 16 * c + 8 * h, true, q[c]);
 
     f32x16 o[S];
-#pragma unroll
-    for (int d = 0; d < S; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
+    float m, l;
+    bool odd_task = false;
 
     // pages of the keys of tiles i .. i + 63, eight keys a page at least
     const auto read_pages = [&](int i) {
@@ -323,12 +344,20 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       const char *k, *v;
     };
     const char* head = reinterpret_cast<const char*>(a.pool + (((int64_t)it.kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0));
-    const auto page_of = [&](int i) { return s_pages[((i - first) & 63) * 8 + (my_key >> 3)]; };
-    const auto source_of = [&](int i, int buf, int page) {
-      const int j0 = it.tl.at(i) << 6, j = j0 + my_key;
-      bool in = (uint32_t)page < (uint32_t)a.num_pages;
-      if (i >= last || j0 + 63 > it.hi || (a.window > 0 && it.lo - j0 >= a.window && j0 + 63 >= a.sinks))
-        in = in && i < last && j <= it.hi && (a.window == 0 || it.lo - j < a.window || j < a.sinks);
+    const auto page_at = [&](int n) { return s_pages[(n & 63) * 8 + (my_key >> 3)]; };  // of the task's n-th tile
+    // first key of the tile after the one from key j
+    const int head_end = it.tl.head << 6, window_start = it.tl.from << 6;
+    const auto next_key = [&](int j) { return j + 64 == head_end ? window_start : j + 64; };
+    // every key of a tile from j is seen by some query if j <= some_hi and (j > some_lo or j <
+    // sinks - 63); by every query likewise
+    const int some_hi = it.hi - 63, all_hi = it.lo - 63, sink_end = a.sinks - 63;
+    const int some_lo = a.window > 0 ? it.lo - a.window : -1, all_lo = a.window > 0 ? it.hi - a.window : -1;
+    const auto source_of = [&](int j0, bool more, int buf, int page) {
+      bool in = more && (uint32_t)page < (uint32_t)a.num_pages;
+      if (!(j0 <= some_hi && (j0 > some_lo || j0 < sink_end))) {
+        const int j = j0 + my_key;
+        in = in && j <= it.hi && (a.window == 0 || it.lo - j < a.window || j < a.sinks);
+      }
       if (W == 4 || wave0 < 4) {
         const unsigned long long there = __ballot(in);
         uint16_t keys = 0xffff;
@@ -336,7 +365,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         if (lane == 0) s_valid[buf][wave0] = keys;
       }
       // a page is at least eight keys long, and a tile starts one or lies in one
-      const char* p = head + (int64_t)(j0 & in_page) * (2 * D) + (uint64_t)(uint32_t)page * page_bytes + my_off;
+      const char* p = head + (uint32_t)((j0 & in_page) * (2 * D)) + ((uint64_t)(uint32_t)page * page_bytes + my_off);
       const char* zero = reinterpret_cast<const char*>(pl.zeros);
       Source x;
       x.k = in ? p : zero;
@@ -344,43 +373,48 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       return x;
     };
     const auto copy_block = [&](const Source& x, int buf, int b) {  // b a constant once unrolled
-      const uint32_t at = buf * (kTile * 16) + b * 4096;
       const auto go = [&](const char* p, uint32_t dst) {
-        if (b == 0) load_lds16<0>(p, dst);
-        else if (b == 1) load_lds16<64>(p, dst);
-        else if (b == 2) load_lds16<128>(p, dst);
-        else load_lds16<192>(p, dst);
+        if (b == 0) load_lds16<0, 0>(p, dst);
+        else if (b == 1) load_lds16<64, 4096>(p, dst);
+        else if (b == 2) load_lds16<128, 8192>(p, dst);
+        else load_lds16<192, 12288>(p, dst);
       };
-      go(x.k, (W == 8 && wave0 >= 4 ? to_v : to_k) + at);
-      if (W == 4) go(x.v, to_v + at);
+      go(x.k, (W == 8 && wave0 >= 4 ? to_v : to_k) + buf * (kTile * 16));
+      if (W == 4) go(x.v, to_v + buf * (kTile * 16));
     };
-    const auto all_see = [&](int j0) {
-      return j0 + 63 <= it.lo && (a.window == 0 || it.hi - j0 < a.window || j0 + 63 < a.sinks);
-    };
-    const auto run_tiles = [&](auto planes) {
+    const auto all_see = [&](int j0) { return j0 <= all_hi && (j0 > all_lo || j0 < sink_end); };
+    const auto run_tiles = [&](auto planes, bool careful) {
     constexpr int NP = decltype(planes)::n;
+#pragma unroll
+    for (int d = 0; d < S; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+    m = -INFINITY;
+    l = 0.0f;
+    if (tid == 0) s_here = s_left = s_odd = 0;
     read_pages(first);
     __syncthreads();
+    int j_now = it.tl.at(first) << 6, j_ahead = j_now;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const Source x = source_of(first + t, t, page_of(first + t));
+    for (int t = 0; t < R - 1; ++t) {
+      const Source x = source_of(j_ahead, first + t < last, t, page_at(t));
+      j_ahead = next_key(j_ahead);
 #pragma unroll
       for (int b = 0; b < S; ++b) copy_block(x, t, b);
     }
-    int buf = 0;
-    for (int i = first; i < last; ++i, buf = buf == 2 ? 0 : buf + 1) {
-      const int j0 = it.tl.at(i) << 6;
-      const int after = buf == 0 ? 2 : buf - 1;  // the buffer that tile i + 2 goes to, free since the last barrier
-      // tile i is here: from the second one on only the copies of the next are under way
-      if (i > first) loads_done<kCopies>();
-      else loads_done<0>();
-      __syncthreads();
-      if (i + 2 < last && ((i + 2 - first) & 63) == 0) {
-        read_pages(i + 2);
+    loads_done<(R - 2) * kCopies>();
+    arrive(&s_here);
+    int buf = 0, here = 0;
+    for (int n = 0; n < last - first; ++n) {
+      const int ahead = n + R - 1, after = (buf + R - 1) & (R - 1);  // the tile to copy, where tile n - 1 was
+      if ((ahead & 63) == 0) {
+        __syncthreads();
+        read_pages(first + ahead);
         __syncthreads();
       }
+      wait_for(&s_here, W * (n + 1), here);
       const u32x2 v2 = *reinterpret_cast<const u32x2*>(s_valid[buf]);
-      const int page = page_of(i + 2);
+      const int page = page_at(ahead);
       __builtin_amdgcn_sched_barrier(0);
       const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
       f32x16 s[2];
@@ -390,7 +424,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c] + t * 128];
+          for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c & 1] + (c >> 1) * 256 + t * 128];
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -408,46 +442,50 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       mfma_settle_before_join();
       const uint64_t valid = ((uint64_t)__builtin_amdgcn_readfirstlane(v2[1]) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(v2[0]);
       // every query of the item sees every key of the tile
-      const bool whole = valid == ~0ull && all_see(j0);
-      if (!whole) {
-        // A weight of 0 does not keep out a value that is infinite or NaN:
-        // such values leave the tile here, and reach the queries that see them
-        // at the item's end.
+      const bool whole = valid == ~0ull && all_see(j_now);
+      if (careful && !whole) {
         for (int at = tid; at < kTile; at += THREADS) {
           u32x4 v = s_v[buf * kTile + at];
-          bool fix = false;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) fix |= !finite_bf16x2(v[e]);
-          if (fix) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
-              if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
-            }
-            s_v[buf * kTile + at] = v;
-            s_bad = 1;
+          for (int e = 0; e < 4; ++e) {
+            if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
+            if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
           }
+          s_v[buf * kTile + at] = v;
         }
         __syncthreads();
       }
-      const Source src = source_of(i + 2, after, page);
+      // this wave's copies of tile i + 1 have landed, those of the tiles after it may be under way
+      loads_done<(R - 3) * kCopies>();
+      arrive(&s_here);
+      const Source src = source_of(j_ahead, first + ahead < last, after, page);
+      const auto advance = [&]() {
+        arrive(&s_left);
+        j_now = next_key(j_now);
+        j_ahead = next_key(j_ahead);
+        buf = (buf + 1) & (R - 1);
+        here = look(&s_here);
+      };
       if (!busy) {
+        wait_for(&s_left, W * n, 0);
 #pragma unroll
         for (int b = 0; b < S; ++b) copy_block(src, after, b);
+        advance();
         continue;
       }
+      const int left = look(&s_left);
       // V of the first two key quarters while the products finish
       bf16x8 vf[2][S];
       const auto read_v = [&](int kc) {
 #pragma unroll
         for (int d = 0; d < S; ++d)
-          vf[kc & 1][d] = join_halves(read_tr(vt, (v_at[d][0] >> 1) + kc * 64, v_at[d][0] & 1),
-                                      read_tr(vt, (v_at[d][1] >> 1) + kc * 64, v_at[d][1] & 1));
+          vf[kc & 1][d] = join_halves(read_tr(vt, v_at[0] + d * 256 + kc * 64, lane & 1), read_tr(vt, v_at[1] + d * 256 + kc * 64, lane & 1));
       };
       read_v(0);
       read_v(1);
       __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
+        const int j0 = j_now;
         uint64_t seen = below(pos - j0 + 1) & valid;
         if (a.window > 0) seen &= ~below((int64_t)pos - a.window + 1 - j0) | below((int64_t)a.sinks - j0);
         seen >>= 4 * h;
@@ -459,12 +497,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
             if (!(w & (1u << (8 * (r >> 2) + (r & 3))))) s[t][r] = -INFINITY;
         }
       }
-      float top = s[0][0];
+      float tops[2] = {s[0][0], s[1][0]};
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int r = 1; r < 16; ++r)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-      top = max_halves(top) * pl.c;
+        for (int t = 0; t < 2; ++t) tops[t] = fmaxf(tops[t], s[t][r]);
+      const float top = max_halves(fmaxf(tops[0], tops[1])) * pl.c;
       // the reference follows only when it is left far behind: weights up to 2^8
       // are as exact, and rescaling costs a pass over o
       if (__any(top > m + 8.0f)) {
@@ -494,9 +532,9 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         }
       };
       weights(0);
-      __builtin_amdgcn_sched_barrier(0);
+      wait_for(&s_left, W * n, left);
       // the next quarter's weights are formed beside this one's products, and
-      // the copies of tile i + 2 spread between them
+      // the copies of the tile ahead spread between them
 #pragma unroll
       for (int kc = 0; kc < 4; ++kc) {
         if (kc < S) copy_block(src, after, kc);
@@ -515,17 +553,36 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      advance();
     }
-    };
-    if constexpr (F32) run_tiles(Planes<3>());
-    else if (few) run_tiles(Planes<2>());
-    else run_tiles(Planes<1>());
     mfma_settle_before_join();
     loads_done<0>();
-    if (tid == 0) s_task = next_task;
-    __syncthreads();  // the next item's first tile goes over a buffer that may still be read
+    };
+    // A weight of 0 does not keep out a value that is infinite or NaN.  Where a
+    // result is not finite, the task is run once more with such values taken out
+    // of the tiles that not every query sees whole; then they are added for the
+    // queries that see them.
+    for (bool careful = false;; careful = true) {
+      if constexpr (F32) run_tiles(Planes<3>(), careful);
+      else if (few) run_tiles(Planes<2>(), careful);
+      else run_tiles(Planes<1>(), careful);
+      bool odd = false;
+#pragma unroll
+      for (int d = 0; d < S; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) odd |= !(fabsf(o[d][r]) < INFINITY);
+      if (tid == 0) s_task = next_task;
+      if (!careful && odd) s_odd = 1;
+      __syncthreads();  // also: the next tiles go over buffers that may still be read
+      const bool again = s_odd != 0 && !careful;
+      __syncthreads();
+      if (!again) {
+        odd_task = careful;
+        break;
+      }
+    }
     task = __builtin_amdgcn_readfirstlane(s_task);
-    if (s_bad) {
+    if (odd_task) {
       for (int j = it.tl.at(first) << 6; j <= it.hi; ++j) {
         const int tile = j >> 6, i = tile < it.tl.head ? tile : tile - it.tl.from + it.tl.head;
         if ((tile >= it.tl.head && tile < it.tl.from) || i < first || i >= last) continue;
@@ -548,7 +605,6 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
           }
       }
     }
-    __syncthreads();
     l += __shfl_xor(l, 32, 64);
     if (it.parts == 1) {
       const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
