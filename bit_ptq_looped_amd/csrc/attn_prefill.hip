@@ -189,37 +189,11 @@ __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
 }
 
-// A barrier in two halves, so that waves may be up to a tile apart: while some
-// form weights, others multiply.  A wave arrives once what it promises is done
-// (LDS operations of a wave keep their order); every wave arrives the same
-// number of times, and what it waits for lies before what others wait for.
-__device__ __forceinline__ void arrive(int* count) {
+// a barrier that waits for LDS operations, but not for copies to LDS under way
+__device__ __forceinline__ void sync_lds() {
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  if ((threadIdx.x & 63) == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-  asm volatile("" ::: "memory");
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-}
-__device__ __forceinline__ int look(int* count) {
-  return __hip_atomic_load(count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-}
-// `seen` is an earlier look, taken where its latency is hidden: counts only grow
-__device__ __forceinline__ void wait_for(int* count, int n, int seen) {
-  __builtin_amdgcn_sched_barrier(0);
-  while (__builtin_amdgcn_readfirstlane(seen) < n) {
-    __builtin_amdgcn_s_sleep(1);
-    seen = look(count);
-  }
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-// whether every key of a tile of 64 has a page
-__device__ __forceinline__ bool tile_has_pages(const AttnArgs& a, const int32_t* table, int tile) {
-  bool ok = true;
-  for (int j = tile << 6; j < (tile + 1) << 6; j += min(64, 1 << a.page_shift))
-    ok &= (uint32_t)table[j >> a.page_shift] < (uint32_t)a.num_pages;
-  return ok;
 }
 
 // A work-group takes a task after another: W waves of 32 rows each over tiles of
@@ -237,10 +211,10 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   constexpr int R = 4;  // buffers of the ring: copies run three tiles ahead
   __shared__ u32x4 s_k[R * kTile], s_v[R * kTile];
   __shared__ __attribute__((aligned(8))) uint16_t s_valid[R][4];  // keys of a tile that some query sees, 16 a wave
-  __shared__ int s_pages[512];  // of 64 tiles' groups of eight keys
+  __shared__ int64_t s_pages[512];  // 64 tiles' groups of eight keys: their place in the pool in bytes, -1 for no page
   __shared__ int s_task;
   __shared__ int s_odd;     // some result is not finite
-  __shared__ int s_here, s_left;  // waves whose copies of a tile have landed; that have left a tile; counted over the task
+  __shared__ int s_paged;   // every group of those 64 tiles that some query sees has a page
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n32 = lane & 31, h = lane >> 5;
   const int in_page = (1 << a.page_shift) - 1;
@@ -258,7 +232,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   // this lane's share of a tile's copy: its key, and a chunk of each block
   const int wave0 = __builtin_amdgcn_readfirstlane(wave);
   const int my_key = (wave0 & 3) * 16 + (lane >> 2);
-  const uint32_t my_off = (my_key & in_page) * (2 * D) + 16 * ((lane & 3) ^ (lane >> 4)), page_bytes = (uint32_t)(2 * a.page_stride);
+  const int my_off = (my_key & 7) * (2 * D) + 16 * ((lane & 3) ^ (lane >> 4));  // bytes from its group of eight keys
   const uint32_t to_k = lds_offset(s_k) + (wave0 & 3) * 1024, to_v = lds_offset(s_v) + (wave0 & 3) * 1024;
   // chunks this lane multiplies
   int k_at[2], v_at[2];  // in the first block; the others follow every 256 chunks
@@ -326,51 +300,57 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     float m, l;
     bool odd_task = false;
 
-    // pages of the keys of tiles i .. i + 63, eight keys a page at least
-    const auto read_pages = [&](int i) {
+    // The tiles of the task by number n.  A tile is copied plainly if every key of
+    // it is seen by some query, and taken whole if every key is seen by every
+    // query; both are runs of numbers (tiles of sinks count as neither), as long as
+    // the pages are there.
+    const int tiles = last - first, shift0 = it.tl.head - it.tl.from - first;  // window tile w is number w + shift0
+    const int64_t low = a.window > 0 ? max((int64_t)it.lo - a.window + 1, (int64_t)0) : 0;
+    const int64_t low_all = a.window > 0 ? max((int64_t)it.hi - a.window + 1, (int64_t)0) : 0;
+    const int plain0 = max((int)((low + 63) >> 6) + shift0, max(it.tl.head - first, 0));
+    const int plain1 = min(((it.hi + 1) >> 6) + shift0, tiles);
+    const int whole0 = max((int)((low_all + 63) >> 6) + shift0, plain0);
+    const int whole1 = min(((it.lo + 1) >> 6) + shift0, tiles);
+
+    // where tiles n .. n + 63 are; barriers on both sides
+    const auto read_pages = [&](int n) {
+      sync_lds();
+      if (tid == 0) s_paged = 1;
+      sync_lds();
       for (int e = tid; e < 512; e += THREADS) {
-        const int t = i + (e >> 3);
-        int page = -1;
-        if (t < last) {
-          const int j = (it.tl.at(t) << 6) + 8 * (e & 7);
-          if (j <= it.hi) page = table[j >> a.page_shift];
+        const int t = n + (e >> 3);
+        int64_t at = -1;
+        if (t < tiles) {
+          const int j = (it.tl.at(first + t) << 6) + 8 * (e & 7);
+          if (j <= it.hi && (j + 7 >= low || j < a.sinks)) {
+            const int page = table[j >> a.page_shift];
+            if ((uint32_t)page < (uint32_t)a.num_pages) at = 2 * (page * a.page_stride + (j & in_page) * D);
+            else s_paged = 0;
+          }
         }
-        s_pages[e] = page;
+        s_pages[e] = at;
       }
+      sync_lds();
+      return __builtin_amdgcn_readfirstlane(s_paged) != 0;
     };
     // where this wave's copies of tile i come from: K and V with four waves, one of
     // them with eight; past the last tile, zeros (so that the loop needs no branch)
     struct Source {
       const char *k, *v;
     };
-    const char* head = reinterpret_cast<const char*>(a.pool + (((int64_t)it.kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0));
-    const auto page_at = [&](int n) { return s_pages[(n & 63) * 8 + (my_key >> 3)]; };  // of the task's n-th tile
-    // first key of the tile after the one from key j
-    const int head_end = it.tl.head << 6, window_start = it.tl.from << 6;
-    const auto next_key = [&](int j) { return j + 64 == head_end ? window_start : j + 64; };
-    // every key of a tile from j is seen by some query if j <= some_hi and (j > some_lo or j <
-    // sinks - 63); by every query likewise
-    const int some_hi = it.hi - 63, all_hi = it.lo - 63, sink_end = a.sinks - 63;
-    const int some_lo = a.window > 0 ? it.lo - a.window : -1, all_lo = a.window > 0 ? it.hi - a.window : -1;
-    const auto source_of = [&](int j0, bool more, int buf, int page) {
-      bool in = more && (uint32_t)page < (uint32_t)a.num_pages;
-      if (!(j0 <= some_hi && (j0 > some_lo || j0 < sink_end))) {
-        const int j = j0 + my_key;
-        in = in && j <= it.hi && (a.window == 0 || it.lo - j < a.window || j < a.sinks);
+    const char* base = reinterpret_cast<const char*>(a.pool + (((int64_t)it.kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0)) + my_off;
+    const int64_t* my_pages = s_pages + (my_key >> 3);
+    const auto plain_source = [&](int64_t at) { return Source{base + at, base + at + (W == 4 ? 2 * a.plane : 0)}; };
+    const auto masked_source = [&](int n, int64_t at, int buf) {
+      bool in = n < tiles && at >= 0;
+      if (in) {
+        const int j = (it.tl.at(first + n) << 6) + my_key;
+        in = j <= it.hi && (j >= low || j < a.sinks);
       }
-      if (W == 4 || wave0 < 4) {
-        const unsigned long long there = __ballot(in);
-        uint16_t keys = 0xffff;
-        if (there != ~0ull) keys = every_fourth(there);
-        if (lane == 0) s_valid[buf][wave0] = keys;
-      }
-      // a page is at least eight keys long, and a tile starts one or lies in one
-      const char* p = head + (uint32_t)((j0 & in_page) * (2 * D)) + ((uint64_t)(uint32_t)page * page_bytes + my_off);
+      const unsigned long long there = __ballot(in);
+      if (lane == 0 && wave0 < 4) s_valid[buf][wave0] = every_fourth(there);
       const char* zero = reinterpret_cast<const char*>(pl.zeros);
-      Source x;
-      x.k = in ? p : zero;
-      x.v = W == 4 && in ? p + 2 * a.plane : zero;
-      return x;
+      return Source{in ? base + at : zero, W == 4 && in ? base + at + 2 * a.plane : zero};
     };
     const auto copy_block = [&](const Source& x, int buf, int b) {  // b a constant once unrolled
       const auto go = [&](const char* p, uint32_t dst) {
@@ -382,7 +362,6 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       go(x.k, (W == 8 && wave0 >= 4 ? to_v : to_k) + buf * (kTile * 16));
       if (W == 4) go(x.v, to_v + buf * (kTile * 16));
     };
-    const auto all_see = [&](int j0) { return j0 <= all_hi && (j0 > all_lo || j0 < sink_end); };
     const auto run_tiles = [&](auto planes, bool careful) {
     constexpr int NP = decltype(planes)::n;
 #pragma unroll
@@ -391,30 +370,23 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
     m = -INFINITY;
     l = 0.0f;
-    if (tid == 0) s_here = s_left = s_odd = 0;
-    read_pages(first);
-    __syncthreads();
-    int j_now = it.tl.at(first) << 6, j_ahead = j_now;
+    if (tid == 0) s_odd = 0;
+    bool paged = read_pages(0), paged_now = paged;  // of the tiles that are copied; that are multiplied
 #pragma unroll
     for (int t = 0; t < R - 1; ++t) {
-      const Source x = source_of(j_ahead, first + t < last, t, page_at(t));
-      j_ahead = next_key(j_ahead);
+      const Source x = masked_source(t, my_pages[t * 8], t);
 #pragma unroll
       for (int b = 0; b < S; ++b) copy_block(x, t, b);
     }
-    loads_done<(R - 2) * kCopies>();
-    arrive(&s_here);
-    int buf = 0, here = 0;
-    for (int n = 0; n < last - first; ++n) {
+    int buf = 0;
+    for (int n = 0; n < tiles; ++n, buf = (buf + 1) & (R - 1)) {
       const int ahead = n + R - 1, after = (buf + R - 1) & (R - 1);  // the tile to copy, where tile n - 1 was
-      if ((ahead & 63) == 0) {
-        __syncthreads();
-        read_pages(first + ahead);
-        __syncthreads();
-      }
-      wait_for(&s_here, W * (n + 1), here);
-      const u32x2 v2 = *reinterpret_cast<const u32x2*>(s_valid[buf]);
-      const int page = page_at(ahead);
+      // this wave's copies of tile n have landed (those of the next two may be under way), then everybody's
+      loads_done<(R - 2) * kCopies>();
+      sync_lds();
+      if ((ahead & 63) == 0) paged = read_pages(ahead);
+      if ((n & 63) == 0) paged_now = paged;
+      const int64_t at = my_pages[(ahead & 63) * 8];
       __builtin_amdgcn_sched_barrier(0);
       const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
       f32x16 s[2];
@@ -440,10 +412,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         __builtin_amdgcn_sched_barrier(0);
       }
       mfma_settle_before_join();
-      const uint64_t valid = ((uint64_t)__builtin_amdgcn_readfirstlane(v2[1]) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(v2[0]);
-      // every query of the item sees every key of the tile
-      const bool whole = valid == ~0ull && all_see(j_now);
-      if (careful && !whole) {
+      const bool whole = paged_now && n >= whole0 && n < whole1;
+      if (careful) {
         for (int at = tid; at < kTile; at += THREADS) {
           u32x4 v = s_v[buf * kTile + at];
 #pragma unroll
@@ -455,25 +425,14 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         }
         __syncthreads();
       }
-      // this wave's copies of tile i + 1 have landed, those of the tiles after it may be under way
-      loads_done<(R - 3) * kCopies>();
-      arrive(&s_here);
-      const Source src = source_of(j_ahead, first + ahead < last, after, page);
-      const auto advance = [&]() {
-        arrive(&s_left);
-        j_now = next_key(j_now);
-        j_ahead = next_key(j_ahead);
-        buf = (buf + 1) & (R - 1);
-        here = look(&s_here);
-      };
+      Source src;
+      if (paged && ahead >= plain0 && ahead < plain1) src = plain_source(at);
+      else src = masked_source(ahead, at, after);
       if (!busy) {
-        wait_for(&s_left, W * n, 0);
 #pragma unroll
         for (int b = 0; b < S; ++b) copy_block(src, after, b);
-        advance();
         continue;
       }
-      const int left = look(&s_left);
       // V of the first two key quarters while the products finish
       bf16x8 vf[2][S];
       const auto read_v = [&](int kc) {
@@ -485,9 +444,11 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       read_v(1);
       __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
-        const int j0 = j_now;
-        uint64_t seen = below(pos - j0 + 1) & valid;
+        const int j0 = it.tl.at(first + n) << 6;
+        uint64_t seen = below(pos - j0 + 1);
         if (a.window > 0) seen &= ~below((int64_t)pos - a.window + 1 - j0) | below((int64_t)a.sinks - j0);
+        // the first tiles of a task are copied by masks, too
+        if (n < R - 1 || !(paged_now && n >= plain0 && n < plain1)) seen &= *reinterpret_cast<const uint64_t*>(s_valid[buf]);
         seen >>= 4 * h;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -532,7 +493,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         }
       };
       weights(0);
-      wait_for(&s_left, W * n, left);
+      __builtin_amdgcn_sched_barrier(0);
       // the next quarter's weights are formed beside this one's products, and
       // the copies of the tile ahead spread between them
 #pragma unroll
@@ -553,15 +514,13 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      advance();
     }
     mfma_settle_before_join();
     loads_done<0>();
     };
     // A weight of 0 does not keep out a value that is infinite or NaN.  Where a
     // result is not finite, the task is run once more with such values taken out
-    // of the tiles that not every query sees whole; then they are added for the
-    // queries that see them.
+    // of the tiles; then they are added for the queries that see them.
     for (bool careful = false;; careful = true) {
       if constexpr (F32) run_tiles(Planes<3>(), careful);
       else if (few) run_tiles(Planes<2>(), careful);
@@ -587,9 +546,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         const int tile = j >> 6, i = tile < it.tl.head ? tile : tile - it.tl.from + it.tl.head;
         if ((tile >= it.tl.head && tile < it.tl.from) || i < first || i >= last) continue;
         const int page = table[j >> a.page_shift];
-        // a tile that every query saw whole kept its values
         if ((uint32_t)page >= (uint32_t)a.num_pages || !sees(a, pos, j)) continue;
-        if (all_see(tile << 6) && tile_has_pages(a, table, tile)) continue;
         const uint16_t* v = a.pool + a.plane + page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < S; ++d)
