@@ -110,7 +110,10 @@ __device__ __forceinline__ int find(const T* p, int n, T u) {
   return lo;
 }
 
-// eight query elements as N bf16 planes of an MFMA operand
+// Eight query elements as N bf16 planes of an MFMA operand.  fp32 has three: the
+// leading bits cut off twice, and the rest, which 8 bits hold.  No plane has
+// another sign than the element, and none is 0 unless the element is (2^-126
+// where nothing is left): all planes times an infinite key are that infinity.
 template <int N>
 __device__ __forceinline__ void load_query(const AttnArgs& a, float mul, int64_t at, bool in, bf16x8 (&q)[N]) {
   float x[8];
@@ -127,12 +130,15 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, float mul, int64_t
     }
   }
 #pragma unroll
-  for (int n = 0; n < N; ++n)
+  for (int e = 0; e < 8; ++e) {
+    const float least = fminf(fabsf(x[e]), 0x1p-126f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      q[n][e] = (__bf16)x[e];
-      x[e] -= (float)q[n][e];
+    for (int n = 0; n < N; ++n) {
+      const float t = n + 1 < N && x[e] == x[e] ? __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u) : x[e];
+      q[n][e] = (__bf16)t;
+      x[e] = copysignf(fabsf(t) == INFINITY ? least : fmaxf(fabsf(x[e] - t), least), t);
     }
+  }
 }
 
 // Eight weights as N bf16 planes: one, rounded to nearest; or the leading bits

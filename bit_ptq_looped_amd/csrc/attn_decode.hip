@@ -242,13 +242,12 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
     u = i0 + last;
   }
   // rows without a visible key belong to no piece
-  if (blockIdx.x == 0)
-    for (int r = 0; r < a.rows; ++r)
-      if (s_prefix[r + 1] == s_prefix[r])
-        for (int d = tid; d < a.heads * a.group * D; d += 256) {
-          if (a.bf16) reinterpret_cast<uint16_t*>(a.out)[r * a.ldo + d] = 0;
-          else reinterpret_cast<float*>(a.out)[r * a.ldo + d] = 0.0f;
-        }
+  for (int r = blockIdx.x; r < a.rows; r += gridDim.x)
+    if (s_prefix[r + 1] == s_prefix[r])
+      for (int d = tid; d < a.heads * a.group * D; d += 256) {
+        if (a.bf16) reinterpret_cast<uint16_t*>(a.out)[r * a.ldo + d] = 0;
+        else reinterpret_cast<float*>(a.out)[r * a.ldo + d] = 0.0f;
+      }
 }
 
 // Short rows: a work-group per item, an eighth of its tiles a wave, joined in

@@ -131,6 +131,42 @@ def test_decode_splits_a_long_row(lq, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("heads,group", [(1, 1), (3, 1), (2, 4), (1, 7), (2, 16), (1, 19), (1, 40)])
+def test_decode_head_layouts_in_a_long_table(lq, dim, heads, group, dtype):
+    """Room for long rows: the work is cut into pieces, whatever the rows' lengths."""
+    Case([45, 1, 0, 130, 16, 700], heads, group, dim, 16, dtype=dtype, width=190).check()
+
+
+@BOTH
+@pytest.mark.parametrize("page", [8, 64, 256])
+def test_decode_lengths_in_a_long_table(lq, page, dtype):
+    Case([0, 1, 2, 15, 16, 17, 31, 33, 64, 65, 127, 128, 129, 255, 257, 300], 2, 2, 96, page, dtype=dtype, width=2600 // page).check()
+
+
+@BOTH
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (17, 4), (64, 64), (300, 5), (30, 1000)])
+def test_decode_window_and_sinks_in_a_long_table(lq, window, sinks, dtype):
+    Case([0, 1, 5, 30, 64, 301, 517, 2011], 2, 3, 64, 16, window, sinks, dtype=dtype, width=140).check()
+
+
+@BOTH
+def test_decode_holes_in_a_long_table(lq, dtype):
+    c = Case([900, 40, 0, 2000, 3], 2, 2, 64, 16, dtype=dtype, width=140, holes=[(0, 2), (0, 55), (1, 0), (1, 1), (1, 2), (3, 12), (3, 124)])
+    c.check()
+    c.check(scale=0.0)
+    c.check(scale=-0.3)
+
+
+@BOTH
+def test_decode_of_mostly_empty_rows(lq, dtype):
+    """Rows of a batch that wait for work: their results are 0."""
+    c = Case([0] * 700 + [900] + [0] * 120, 1, 2, 64, 16, dtype=dtype, width=140)
+    out = c.check(some=30)
+    assert not out[:700].any() and not out[701:].any()
+
+
+@BOTH
 def test_decode_many_rows(lq, dtype):
     rng = random.Random(2)
     Case([rng.randint(0, 400) for _ in range(333)], 2, 1, 64, 16, dtype=dtype).check(some=60)
@@ -179,6 +215,13 @@ def test_prefill_larger(lq, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5000, 70)])
+def test_prefill_walks_many_tiles(lq, window, sinks, dtype):
+    """Work-groups that go over more than 64 tiles of keys each, with pages missing."""
+    Case([6100], 1, 40, 64, 16, window, sinks, dtype=dtype, news=[1500], holes=[(0, 3), (0, 200), (0, 301)]).check(some=25)
+
+
+@BOTH
 def test_more_queries_than_tokens(lq, dtype):
     """Queries at negative positions see nothing: 0."""
     c = Case([5, 40], 1, 2, 64, 16, dtype=dtype, news=[9, 40])
@@ -224,6 +267,21 @@ def test_a_value_hidden_from_the_only_query(lq, dtype):
     want = c.check().clone()
     for j in (2, 100, 159):
         c.pool[c.table[0][j // 16], c.slab, :, :, j % 16] = math.inf
+    assert torch.equal(c.run(), want)
+
+
+@BOTH
+@pytest.mark.parametrize("width", [13, 140])
+@pytest.mark.parametrize("news", [None, [1]])
+def test_a_key_of_minus_infinity(lq, news, width, dtype):
+    """A score of -infinity is a weight of 0, as a score of -1e30 is."""
+    c = Case([200], 1, 1, 64, 16, dtype=dtype, news=news, width=width)
+    for j in (0, 77, 199):
+        c.pool[c.table[0][j // 16], c.slab, 0, 0, j % 16, 9] = -1e30 * torch.sign(c.q[0, 0, 9])
+    want = c.run()
+    assert torch.isfinite(want).all()
+    for j in (0, 77, 199):
+        c.pool[c.table[0][j // 16], c.slab, 0, 0, j % 16, 9] = -math.inf * torch.sign(c.q[0, 0, 9])
     assert torch.equal(c.run(), want)
 
 

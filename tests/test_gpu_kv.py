@@ -148,7 +148,7 @@ def test_fork_to_no_rows_frees_everything(lq):
 @pytest.mark.parametrize("inplace", [False, True])
 @pytest.mark.parametrize("rows,width,pages,page,window,sinks", [
     (1, 1, 1, 8, 1, 0), (5, 12, 80, 16, 1, 0), (5, 12, 80, 16, 33, 17), (40, 30, 1400, 32, 100, 4), (6, 9, 99, 8, 1000, 5),
-    (9, 40, 400, 16, 16, 16)])
+    (9, 40, 400, 16, 16, 16), (100, 200, 3000, 16, 300, 40)])
 def test_trim(lq, rows, width, pages, page, window, sinks, inplace):
     rng = random.Random(rows + window)
     table, lens, refs = state(rng, rows, width, pages, page, shared=True)
@@ -328,3 +328,20 @@ def test_bookkeeping_in_a_graph(lq):
         pool.copy_(first)
         step()
         assert host(b) == want and same_bits(pool, eager)
+
+
+def test_timing_hooks_count_calls(lq):
+    from bit_ptq_looped_amd import loopq
+    pool = make_pool(8, 1, 1, 16, 64)
+    pool.zero_()
+    t = dev_table([[3, -1], [5, -1]], [9, 16], [0, 0, 0, 1, 0, 1, 0, 0], 2)
+    info, q = torch.empty(2, dtype=torch.int32, device="cuda"), torch.zeros((2, 2, 64), device="cuda")
+    loopq.loopq_timing_reset()
+    loopq.loopq_timing_enable(True)
+    kv.loopq_kv_reserve(t, 16, i32([1, 1]), t, info, kv.empty_pages_workspace(2, 8))
+    kv.loopq_kv_trim(t, 16, 8, 0, t)
+    kv.loopq_attn_decode(pool, 0, t, q, torch.empty_like(q), kv.empty_attn_workspace(pool, 2, 2, 2), 1.0)
+    loopq.loopq_timing_enable(False)
+    times = loopq.loopq_timing_read()
+    assert times[loopq.LOOPQ_KERNEL_KV][1] == 2 and times[loopq.LOOPQ_KERNEL_ATTN][1] == 1
+    assert times[loopq.LOOPQ_KERNEL_KV][0] > 0 and times[loopq.LOOPQ_KERNEL_ATTN][0] > 0

@@ -55,7 +55,8 @@ def test_sizes(lib):
 @pytest.mark.parametrize("kw,want", [
     (dict(head_dim=80), UNSUPPORTED), (dict(head_dim=0), INVALID), (dict(page_size=12), UNSUPPORTED), (dict(page_size=4), UNSUPPORTED),
     (dict(page_size=512), UNSUPPORTED), (dict(page_size=0), INVALID), (dict(num_pages=0), INVALID), (dict(num_pages=(1 << 22) + 1), UNSUPPORTED),
-    (dict(slabs=0), INVALID), (dict(heads=-1), INVALID), (dict(data=None), INVALID), (dict(data=FAKE + 8), ALIGNMENT)])
+    (dict(slabs=1 << 14, heads=64, page_size=256, head_dim=128), UNSUPPORTED), (dict(slabs=1, heads=1 << 15), UNSUPPORTED),
+    (dict(slabs=(1 << 16) + 1, heads=1), UNSUPPORTED), (dict(slabs=0), INVALID), (dict(heads=-1), INVALID), (dict(data=None), INVALID), (dict(data=FAKE + 8), ALIGNMENT)])
 def test_pools_are_checked(lib, kw, want):
     p, t, u = pool(**kw), table(), table(OTHER)
     n = p.num_pages if 0 < p.num_pages <= 1 << 22 else 8
@@ -159,5 +160,7 @@ def test_attention_arguments(lib, prefill):
     if prefill:
         assert call(cu=None) == INVALID and call(cu=FAKE + 2) == ALIGNMENT and call(n=-1) == INVALID
         assert call(n=0, q=None, out=None) == 0
+        assert call(n=(1 << 31) - 1, hq=4096, ldq=1 << 18, ldo=1 << 18) == UNSUPPORTED  # query tiles are counted in 32 bits
+    assert call(hq=1 << 15) == UNSUPPORTED
     t.rows = 0
     assert call(q=None, out=None) == 0
