@@ -31,8 +31,8 @@ namespace loopq {
 namespace {
 
 struct AttnSizes {
-  size_t part, ml, records, row, tile;
-  size_t all() const { return part + ml + records + 3 * row + 2 * tile + 512; }
+  size_t part, ml, records, row, tasks;
+  size_t all() const { return part + ml + records + row + tasks + 512; }
 };
 size_t up256(int64_t b) { return (size_t)((b + 255) / 256 * 256); }
 AttnSizes attn_sizes(int64_t queries, int heads_q, int64_t rows, int D) {
@@ -42,7 +42,8 @@ AttnSizes attn_sizes(int64_t queries, int heads_q, int64_t rows, int D) {
   s.ml = up256(n * 2 * 4);
   s.records = up256(max(kDecodePieces, kPrefillSlots) * sizeof(JoinRecord));
   s.row = up256((rows + 1) * 4);
-  s.tile = up256((queries * heads_q / 128 + rows + 1) * 4);  // tiles of 128 rows at least
+  // query tiles have 128 rows at least, and are split into 256 parts more at most
+  s.tasks = up256((queries * heads_q / 128 + rows + kPrefillGroups) * sizeof(PrefillTask));
   return s;
 }
 
@@ -60,11 +61,9 @@ hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
   pl.ml = reinterpret_cast<float*>(p += z.part);
   pl.records = reinterpret_cast<JoinRecord*>(p += z.ml);
   pl.row_tiles = reinterpret_cast<int32_t*>(p += z.records);
-  pl.row_task = reinterpret_cast<int32_t*>(p += z.row);
-  pl.row_slot = reinterpret_cast<int32_t*>(p += z.row);
-  pl.tile_task = reinterpret_cast<int32_t*>(p += z.row);
-  pl.tile_slot = reinterpret_cast<int32_t*>(p += z.tile);
-  pl.zeros = reinterpret_cast<uint16_t*>(p += z.tile);
+  pl.tasks = reinterpret_cast<PrefillTask*>(p += z.row);
+  pl.most_tiles = (int32_t)(z.tasks / sizeof(PrefillTask)) - kPrefillGroups;
+  pl.zeros = reinterpret_cast<uint16_t*>(p += z.tasks);
   pl.head = reinterpret_cast<int32_t*>(p += 256);
   pl.next = reinterpret_cast<int32_t*>(p + 64);
   // t = s c with c > 0, so that the largest score has the largest t

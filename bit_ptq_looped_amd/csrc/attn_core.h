@@ -32,18 +32,26 @@ struct JoinRecord {
   int32_t parts, row, item, tile;
 };
 
+// A prefill task: key tiles k0 .. k1 - 1 of a query tile, for one key head.
+struct PrefillTask {
+  int32_t row, first, n, len;   // the row, its first query, its queries, its tokens
+  int32_t tile, lo, hi;         // the query tile, positions of its first and last query
+  int32_t head, from;           // its key tiles: `head` from 0, then from `from` on
+  int32_t k0, k1;
+  int32_t part, parts, slot;    // of the item: this part, all, the first one's slot if there are several
+  int32_t pad[2];
+};
+
 // what a launch needs beside the caller's arguments
 struct AttnPlan {
   float* part;            // partial results: [slot][rows][head_dim], then
   float* ml;              // their m and l: [slot][2][rows]
   JoinRecord* records;
   int32_t* row_tiles;     // prefill: query tiles before each row, [rows + 1]
-  int32_t* row_task;      // prefill: tasks before each row, [rows + 1]
-  int32_t* row_slot;      // prefill: slots before each row, [rows + 1]
-  int32_t* tile_task;     // prefill: tasks of one key head before each query tile
-  int32_t* tile_slot;     // the same for slots
-  int32_t* head;          // prefill: {most key tiles of a task, key heads of a block}
+  PrefillTask* tasks;     // prefill: the tasks of one key head
+  int32_t* head;          // prefill: {tasks of a key head, slots of a key head, key heads of a block}
   int32_t* next;          // tasks handed out, of each eighth of the tasks
+  int32_t most_tiles;     // prefill: query tiles, at most
   const uint16_t* zeros;  // 256 zero bytes, cleared by the plan launch
   float c;                // |scale| log2(e), or 1 for a scale of 0
   float qmul;             // sign of the scale: queries are taken times this
@@ -115,30 +123,28 @@ __device__ __forceinline__ int find(const T* p, int n, T u) {
 // another sign than the element, and none is 0 unless the element is (2^-126
 // where nothing is left): all planes times an infinite key are that infinity.
 template <int N>
-__device__ __forceinline__ void load_query(const AttnArgs& a, float mul, int64_t at, bool in, bf16x8 (&q)[N]) {
-  float x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-  if (in) {
-    if (N == 1) {
-      const u32x4 u = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + at);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = mul * bf16_bits_to_float(e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xffffu);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = mul * reinterpret_cast<const float*>(a.q)[at + e];
-    }
-  }
+__device__ __forceinline__ void query_planes(const u32x4 (&raw)[N == 1 ? 1 : 2], float mul, bf16x8 (&q)[N]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float least = fminf(fabsf(x[e]), 0x1p-126f);
+    float x = mul * (N == 1 ? bf16_bits_to_float(e & 1 ? raw[0][e >> 1] >> 16 : raw[0][e >> 1] & 0xffffu) : __uint_as_float(raw[N > 1 ? e >> 2 : 0][e & 3]));
+    const float least = fminf(fabsf(x), 0x1p-126f);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const float t = n + 1 < N && x[e] == x[e] ? __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u) : x[e];
+      const float t = n + 1 < N && x == x ? __uint_as_float(__float_as_uint(x) & 0xffff0000u) : x;
       q[n][e] = (__bf16)t;
-      x[e] = copysignf(fabsf(t) == INFINITY ? least : fmaxf(fabsf(x[e] - t), least), t);
+      x = copysignf(fabsf(t) == INFINITY ? least : fmaxf(fabsf(x - t), least), t);
     }
   }
+}
+template <int N>
+__device__ __forceinline__ void load_query(const AttnArgs& a, float mul, int64_t at, bool in, bf16x8 (&q)[N]) {
+  u32x4 raw[N == 1 ? 1 : 2];
+#pragma unroll
+  for (int x = 0; x < (N == 1 ? 1 : 2); ++x) {
+    raw[x] = u32x4{0, 0, 0, 0};
+    if (in) raw[x] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(a.q) + at * (N == 1 ? 2 : 4) + 16 * x);
+  }
+  query_planes(raw, mul, q);
 }
 
 // Eight weights as N bf16 planes: one, rounded to nearest; or the leading bits

@@ -24,21 +24,6 @@ __device__ __forceinline__ float max_halves(float v) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// The last i in [0, n) with p[i] <= x (p[0] <= x, p ascending), by the whole
-// wave: 64 places at a time, since a place costs a trip to memory.
-__device__ __forceinline__ int find_wave(const int32_t* p, int n, int x) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, step;
-  do {
-    step = (n - lo + 63) >> 6;
-    const int i = lo + lane * step;
-    const int below = __popcll(__ballot(i < n && p[min(i, n - 1)] <= x)) - 1;
-    lo += below * step;
-    n = min(n, lo + step);
-  } while (step > 1);
-  return lo;
-}
-
 // exclusive sum over 1024 threads, and the sum of all; `part` is 16 values of scratch
 __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* part, int64_t* all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -64,7 +49,8 @@ __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* part, int64_t*
 // One work-group.  A task is an item or, where an item has more than L key
 // tiles, a part of it of at most L; L is a work-group's even share of all key
 // tiles, so that few long items are split over the whole chip and many stay
-// whole.  Slots take the results of split items' tasks: at most 2 tiles / L.
+// whole.  Slots take the results of split items' tasks: at most 2 tiles / L.  All
+// key heads have the same tasks; they are written down once.
 template <int ROWS>
 __global__ __launch_bounds__(1024) void prefill_plan_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ int64_t part[16];
@@ -72,97 +58,97 @@ __global__ __launch_bounds__(1024) void prefill_plan_kernel(AttnArgs a, AttnPlan
   const int tid = threadIdx.x;
   if (tid < 64) reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(pl.zeros))[tid] = 0;
   if (tid < 8) pl.next[tid] = 0;
-  int64_t T = 0, all;
+  int64_t T = 0, all;  // query tiles; only an order of cu that is not ascending gives more than there is room for
   for (int r0 = 0; r0 < a.rows; r0 += 1024) {
     const int r = r0 + tid;
     int first;
     const int n = r < a.rows ? query_tiles<ROWS>(a, row_queries(a, r, &first)) : 0;
-    const int64_t at = T + sum_before(n, part, &all);
+    const int64_t at = min(T + sum_before(n, part, &all), (int64_t)pl.most_tiles);
     if (r < a.rows) {
       pl.row_tiles[r] = (int32_t)at;
       if (r < 1024) s_rows[r] = (int32_t)at;
     }
-    T += all;
-  }
-  if (tid == 0) {
-    pl.row_tiles[a.rows] = (int32_t)T;
-    if (a.rows < 1025) s_rows[a.rows] = (int32_t)T;
+    T = min(T + all, (int64_t)pl.most_tiles);
   }
   __syncthreads();
   const int32_t* row_tiles = a.rows <= 1024 ? s_rows : pl.row_tiles;
-  const auto keys_of = [&](int t) {
-    const int row = find(row_tiles, a.rows, t);
-    int first, lo, hi;
-    const int n = row_queries(a, row, &first);
-    return tile_keys<ROWS>(a, t - row_tiles[row], n, row_len(a, row), &lo, &hi).n;
+  const auto item_of = [&](int t, Tiles* tl) {
+    PrefillTask x;
+    x.row = find(row_tiles, a.rows, t);
+    x.n = row_queries(a, x.row, &x.first);
+    x.len = row_len(a, x.row);
+    x.tile = t - row_tiles[x.row];
+    *tl = tile_keys<ROWS>(a, x.tile, x.n, x.len, &x.lo, &x.hi);
+    x.head = tl->head;
+    x.from = tl->from;
+    return x;
   };
   int64_t keys = 0;
-  int mine = 0;  // key tiles of query tile tid: most calls have no more than 1024
+  PrefillTask mine;  // query tile tid: most calls have no more than 1024
+  Tiles mine_tl{0, 0, 0};
   for (int64_t t = tid; t < T; t += 1024) {
-    const int n = keys_of((int)t);
-    if (t < 1024) mine = n;
-    keys += n;
+    Tiles tl;
+    const PrefillTask x = item_of((int)t, &tl);
+    if (t < 1024) {
+      mine = x;
+      mine_tl = tl;
+    }
+    keys += tl.n;
   }
   sum_before(keys, part, &all);
   const int64_t L = max((int64_t)4, (all * a.heads + kPrefillGroups - 1) / kPrefillGroups);
   int64_t base = 0;  // tasks in the low half, slots in the high one
   for (int64_t t0 = 0; t0 < T; t0 += 1024) {
     const int64_t t = t0 + tid;
-    const int64_t n = t < T ? (t < 1024 ? mine : keys_of((int)t)) : 0, parts = (n + L - 1) / L;
+    Tiles tl{0, 0, 0};
+    PrefillTask x;
+    if (t < 1024) {
+      x = mine;
+      tl = mine_tl;
+    } else if (t < T) {
+      x = item_of((int)t, &tl);
+    }
+    const int64_t parts = (tl.n + L - 1) / L;
     const int64_t at = base + sum_before(parts + (parts > 1 ? parts << 32 : 0), part, &all);
-    if (t < T) {
-      pl.tile_task[t] = (int32_t)at;
-      pl.tile_slot[t] = (int32_t)(at >> 32);
+    x.parts = (int32_t)parts;
+    x.slot = (int32_t)(at >> 32);
+    for (int i = 0; i < (int)parts; ++i) {
+      x.part = i;
+      x.k0 = (int32_t)(i * L);
+      x.k1 = (int32_t)min((i + 1) * L, (int64_t)tl.n);
+      x.pad[0] = x.pad[1] = 0;
+      pl.tasks[(int32_t)at + i] = x;
     }
     base += all;
   }
-  __syncthreads();
-  for (int r = tid; r <= a.rows; r += 1024) {
-    const int t = r < a.rows ? row_tiles[r] : (int)T;
-    pl.row_task[r] = a.heads * (t < T ? pl.tile_task[t] : (int32_t)base);
-    pl.row_slot[r] = a.heads * (t < T ? pl.tile_slot[t] : (int32_t)(base >> 32));
-  }
   if (tid == 0) {
-    pl.head[0] = (int32_t)min(L, (int64_t)0x7fffffff);
-    pl.head[1] = min(max(a.heads * a.rows / 8, 1), a.heads);
+    pl.head[0] = (int32_t)base;
+    pl.head[1] = (int32_t)(base >> 32);
+    pl.head[2] = min(max(a.heads * a.rows / 8, 1), a.heads);
   }
 }
 
-struct PrefillItem {
-  int row, kvh, tile, part, parts, n, len, first;  // first: the row's first query
-  int lo, hi;                                      // positions of the tile's queries
-  Tiles tl;
-  int from, to;                                    // key tiles of the task
-  int slot;                                        // of the item's first task, if there are several
-};
-// Task x.  A row's key heads come in blocks, as many as share an XCD; in a block
-// the query tiles go from the last, which has the most keys, to the first, each
-// for every head: work-groups that run together read the same keys, and what is
-// handed out at the end is short.
-template <int ROWS>
-__device__ __forceinline__ PrefillItem prefill_item(const AttnArgs& a, const AttnPlan& pl, int x) {
-  PrefillItem it;
-  it.row = find_wave(pl.row_task, a.rows, x);
-  it.n = row_queries(a, it.row, &it.first);
-  it.len = row_len(a, it.row);
-  const int L = pl.head[0], block = pl.head[1];
-  const int t0 = pl.row_tiles[it.row], t1 = pl.row_tiles[it.row + 1];
-  const int task0 = pl.row_task[it.row], per = (pl.row_task[it.row + 1] - task0) / a.heads;
-  const int slot0 = pl.row_slot[it.row], slots = (pl.row_slot[it.row + 1] - slot0) / a.heads;
-  x -= task0;
-  const int b = x / (block * per), heads = min(block, a.heads - b * block);
-  x -= b * block * per;
+// Task x of Z for each of the key heads.  Heads come in blocks, as many as share
+// an XCD; in a block the tasks of a head go from the last, since a row's last
+// query tile has the most keys, to the first, each for every head: work-groups
+// that run together read the same keys, and what is handed out at the end is
+// short.
+__device__ __forceinline__ int which_task(const AttnArgs& a, int Z, int block, int x, int* kvh) {
+  const int b = x / (block * Z), heads = min(block, a.heads - b * block);
+  x -= b * block * Z;
   const int y = x / heads;
-  it.kvh = b * block + x - y * heads;
-  const int z = task0 / a.heads + per - 1 - y;
-  it.tile = find_wave(pl.tile_task + t0, t1 - t0, z);
-  it.part = z - pl.tile_task[t0 + it.tile];
-  it.slot = slot0 + it.kvh * slots + pl.tile_slot[t0 + it.tile] - slot0 / a.heads;
-  it.tl = tile_keys<ROWS>(a, it.tile, it.n, it.len, &it.lo, &it.hi);
-  it.parts = (int)(((int64_t)it.tl.n + L - 1) / L);
-  it.from = (int)((int64_t)it.part * L);
-  it.to = (int)min(((int64_t)it.part + 1) * L, (int64_t)it.tl.n);
-  return it;
+  *kvh = b * block + x - y * heads;
+  return Z - 1 - y;
+}
+
+// a task that lies in LDS, for the whole wave
+__device__ __forceinline__ PrefillTask read_task(const PrefillTask& t) {
+  PrefillTask r;
+  const int32_t* from = reinterpret_cast<const int32_t*>(&t);
+  int32_t* to = reinterpret_cast<int32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) to[i] = __builtin_amdgcn_readfirstlane(from[i]);
+  return r;
 }
 
 // 16 bytes per lane from src + OFF (bytes, per lane) to LDS at byte dst + DST +
@@ -175,6 +161,10 @@ __device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
   asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(dst), "v"(src), "n"(OFF),
                "n"(DST - OFF)
                : "memory", "m0", "scc");
+}
+// 4 bytes per lane to LDS at byte dst + 4 lane, in the same manner
+__device__ __forceinline__ void load_lds4(const void* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(dst), "v"(src) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
@@ -198,9 +188,11 @@ __device__ __forceinline__ void sync_lds() {
 
 // A work-group takes a task after another: W waves of 32 rows each over tiles of
 // 64 keys, K and V of the next three tiles on their way to a ring of four
-// buffers in LDS while one is multiplied.  Keys that no query of the item sees are read
-// from a line of zeros.  fp32 queries hold three planes in registers and take
-// half the rows.
+// buffers in LDS while one is multiplied.  The next task is asked for, and its
+// description and page entries fetched, during the last three tiles, and its first
+// tiles are on their way while results are stored.  Keys that no query of the item
+// sees are read from a line of zeros.  fp32 queries hold three planes in registers
+// and take half the rows.
 template <int D, bool F32, int W>
 __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a, AttnPlan pl) {
   constexpr int NQ = F32 ? 3 : 1;
@@ -212,13 +204,16 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   __shared__ u32x4 s_k[R * kTile], s_v[R * kTile];
   __shared__ __attribute__((aligned(8))) uint16_t s_valid[R][4];  // keys of a tile that some query sees, 16 a wave
   __shared__ int64_t s_pages[512];  // 64 tiles' groups of eight keys: their place in the pool in bytes, -1 for no page
-  __shared__ int s_task;
+  __shared__ int s_entry[512];      // the next task's page entries
+  __shared__ PrefillTask s_tasks[2];  // the task at work and the next one, in turn
+  __shared__ int s_task, s_head;    // its number, or -1; its key head
   __shared__ int s_odd;     // some result is not finite
   __shared__ int s_paged;   // every group of those 64 tiles that some query sees has a page
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n32 = lane & 31, h = lane >> 5;
   const int in_page = (1 << a.page_shift) - 1;
-  const int64_t tasks = pl.row_task[a.rows];
+  const int Z = pl.head[0], block = pl.head[2];
+  const int64_t tasks = (int64_t)Z * a.heads;
   // Work-groups go round the eight XCDs; each XCD has an eighth of the tasks
   // (neighbours share keys, and with them an L2), a first one per work-group and
   // the rest in turn, then helps out in the other eighths.  Which work-group
@@ -226,7 +221,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   constexpr int kPer = kPrefillGroups / 8;
   const int eighth = blockIdx.x & 7;
   const auto start_of = [&](int e) { return (int)(tasks * e / 8); };
-  int task = start_of(eighth) + (int)(blockIdx.x >> 3);
+  const int own = start_of(eighth) + kPer, own_left = start_of(eighth + 1) - own;
+  int task = own - kPer + (int)(blockIdx.x >> 3);
   if (task >= start_of(eighth + 1)) task = -1;
 
   // this lane's share of a tile's copy: its key, and a chunk of each block
@@ -234,6 +230,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   const int my_key = (wave0 & 3) * 16 + (lane >> 2);
   const int my_off = (my_key & 7) * (2 * D) + 16 * ((lane & 3) ^ (lane >> 4));  // bytes from its group of eight keys
   const uint32_t to_k = lds_offset(s_k) + (wave0 & 3) * 1024, to_v = lds_offset(s_v) + (wave0 & 3) * 1024;
+  const int64_t* my_pages = s_pages + (my_key >> 3);
   // chunks this lane multiplies
   int k_at[2], v_at[2];  // in the first block; the others follow every 256 chunks
 #pragma unroll
@@ -244,284 +241,349 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     v_at[e] = chunk_at<6, false>(4 * h + 8 * e + (x >> 2), 2 * (g & 1) + ((x & 3) >> 1));
   }
 
-  for (;;) {
-    if (task < 0 && wave0 == 0) {  // what the other eighths have left
-      int found = -1;
-      uint64_t open = 0xff;  // a try that fails closes an eighth for good: nine rounds at most
-      for (;;) {
-        const int e = (eighth + lane) & 7;
-        const int left = max(start_of(e + 1) - start_of(e) - kPer, 0);
-        const int taken = __hip_atomic_load(pl.next + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        open &= __ballot(lane < 8 && taken < left);
-        if (open == 0) break;
-        const int at = __ffsll((unsigned long long)open) - 1, f = (eighth + at) & 7;
-        int x = lane == 0 ? atomicAdd(pl.next + f, 1) : 0;
-        x = __builtin_amdgcn_readfirstlane(x);
-        if (x < start_of(f + 1) - start_of(f) - kPer) {
-          found = start_of(f) + kPer + x;
-          break;
-        }
-        open &= ~(1ull << at);
+  int turn = 0, kvh = 0;  // the task at work is s_tasks[turn]: scalar registers are short
+  // Its tiles by number n.  A tile is copied plainly if every key of it is seen by
+  // some query, and taken whole if every key is seen by every query; both are
+  // runs of numbers (tiles of sinks count as neither), as long as the pages are
+  // there.
+  int tiles, k0, head, from, hi, low;  // low: the first key in some query's window
+  int plain0, plain1, whole0, whole1;
+  const char* base;  // this lane's first byte of its key head's keys or values in page 0
+  bool paged;        // of the tiles that are copied
+  bool few, busy;    // few keys a query; the wave has rows
+  int pos;           // of this lane's query
+  u32x4 qraw[D / 16][F32 ? 2 : 1];
+
+  const auto key_in = [&](int k0, int head, int from, int n) {  // first key of tile n of a task
+    const int i = k0 + n;
+    return (i < head ? i : from + i - head) << 6;
+  };
+  const auto key_of = [&](int n) { return key_in(k0, head, from, n); };
+  const auto in_window = [&](int p) { return a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0; };  // first key
+  // some query sees a key of group j .. j + 7 (of those up to hi)
+  const auto any_sees = [&](int j, int hi, int low) { return j <= hi && (j + 7 >= low || j < a.sinks); };
+  // places of tiles n .. n + 63, from the table or from the entries fetched; barriers on both sides
+  const auto read_pages = [&](int n, bool fetched) {
+    sync_lds();
+    if (tid == 0) s_paged = 1;
+    sync_lds();
+    const int32_t* table = a.table + (int64_t)__builtin_amdgcn_readfirstlane(s_tasks[turn].row) * a.width;
+    for (int e = tid; e < 512; e += THREADS) {
+      const int i = n + (e >> 3), j = key_of(i) + 8 * (e & 7);
+      int64_t at = -1;
+      if (i < tiles && any_sees(j, hi, low)) {
+        const int page = fetched ? s_entry[e] : table[j >> a.page_shift];
+        if ((uint32_t)page < (uint32_t)a.num_pages) at = 2 * (page * a.page_stride + (j & in_page) * D);
+        else s_paged = 0;
       }
-      if (lane == 0) s_task = found;
+      s_pages[e] = at;
     }
-    if (task < 0) {
-      __syncthreads();
-      task = __builtin_amdgcn_readfirstlane(s_task);
-      if (task < 0) return;
+    sync_lds();
+    return __builtin_amdgcn_readfirstlane(s_paged) != 0;
+  };
+  // where this wave's copies of tile i come from: K and V with four waves, one of
+  // them with eight; past the last tile, zeros (so that the loop needs no branch)
+  struct Source {
+    const char *k, *v;
+  };
+  const auto plain_source = [&](int64_t at) { return Source{base + at, base + at + (W == 4 ? 2 * a.plane : 0)}; };
+  const auto masked_source = [&](int n, int64_t at, int buf) {
+    bool in = n < tiles && at >= 0;
+    if (in) {
+      const int j = key_of(n) + my_key;
+      in = j <= hi && (j >= low || j < a.sinks);
     }
-    const PrefillItem it = prefill_item<ROWS>(a, pl, task);
-    const int first = it.from, last = it.to;
-    // the eighth's next task, while this one runs
-    const int own_left = start_of(eighth + 1) - start_of(eighth) - kPer;
-    int next_task = -1;
-    if (tid == 0 && own_left > 0) {
-      const int x = atomicAdd(pl.next + eighth, 1);
-      if (x < own_left) next_task = start_of(eighth) + kPer + x;
-    }
-    const int32_t* table = a.table + (int64_t)it.row * a.width;
-    const int64_t rows = (int64_t)it.n * a.group;
-    const int64_t rr = (int64_t)it.tile * ROWS + wave * 32 + n32;
-    const bool busy = (int64_t)it.tile * ROWS + wave0 * 32 < rows;  // the wave has rows
-    const bool has = rr < rows;
-    const int64_t rq = has ? rr : rows - 1;
-    const int qi = (int)(rq / a.group), hq = it.kvh * a.group + (int)(rq - (int64_t)qi * a.group);
-    const int pos = it.len - it.n + qi;  // position of this lane's query
+    const unsigned long long there = __ballot(in);
+    if (lane == 0 && wave0 < 4) s_valid[buf][wave0] = every_fourth(there);
+    const char* zero = reinterpret_cast<const char*>(pl.zeros);
+    return Source{in ? base + at : zero, W == 4 && in ? base + at + 2 * a.plane : zero};
+  };
+  const auto copy_block = [&](const Source& x, int buf, int b) {  // b a constant once unrolled
+    const auto go = [&](const char* p, uint32_t dst) {
+      if (b == 0) load_lds16<0, 0>(p, dst);
+      else if (b == 1) load_lds16<64, 4096>(p, dst);
+      else if (b == 2) load_lds16<128, 8192>(p, dst);
+      else load_lds16<192, 12288>(p, dst);
+    };
+    go(x.k, (W == 8 && wave0 >= 4 ? to_v : to_k) + buf * (kTile * 16));
+    if (W == 4) go(x.v, to_v + buf * (kTile * 16));
+  };
+  // this lane's row of a task: its query, head and position
+  struct Row {
+    bool has;
+    int qi, hq, pos;
+  };
+  const auto row_of = [&](const PrefillTask& t, int kvh) {
+    const int64_t rows = (int64_t)t.n * a.group, rr = (int64_t)t.tile * ROWS + wave * 32 + n32;
+    const int64_t rq = min(rr, rows - 1);
+    Row r;
+    r.has = rr < rows;
+    r.qi = (int)(rq / a.group);
+    r.hq = kvh * a.group + (int)(rq - (int64_t)r.qi * a.group);
+    r.pos = t.len - t.n + r.qi;
+    return r;
+  };
+  // queries and first tiles of `it` on their way; no copy may be under way
+  const auto start = [&](bool fetched) {
+    const PrefillTask t = read_task(s_tasks[turn]);
+    tiles = t.k1 - t.k0;
+    k0 = t.k0;
+    head = t.head;
+    from = t.from;
+    hi = t.hi;
+    low = in_window(t.lo);
+    const int low_all = in_window(t.hi), shift0 = t.head - t.from - t.k0;  // window tile w is number w + shift0
+    plain0 = max(((low + 63) >> 6) + shift0, max(head - k0, 0));
+    plain1 = min(((hi + 1) >> 6) + shift0, tiles);
+    whole0 = max(((low_all + 63) >> 6) + shift0, plain0);
+    whole1 = min(((t.lo + 1) >> 6) + shift0, tiles);
     // bf16 weights are rounded by up to 2^-8 of themselves; over many keys that
     // averages out, with few the weights take a second plane
-    const bool few = !F32 && (it.lo < 255 || (a.window > 0 && a.window < 256));
-
-    bf16x8 q[D / 16][NQ];
+    few = !F32 && (t.lo < 255 || (a.window > 0 && a.window < 256));
+    base = reinterpret_cast<const char*>(a.pool + (((int64_t)kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0)) + my_off;
+    const Row r = row_of(t, kvh);
+    pos = r.pos;
+    busy = (int64_t)t.tile * ROWS + wave0 * 32 < (int64_t)t.n * a.group;
+    const int64_t q0 = (int64_t)(t.first + r.qi) * a.ldq + (int64_t)r.hq * D + 8 * h;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
-      load_query<NQ>(a, pl.qmul, (int64_t)(it.first + qi) * a.ldq + (int64_t)hq * D + 16 * c + 8 * h, true, q[c]);
-
-    f32x16 o[S];
-    float m, l;
-    bool odd_task = false;
-
-    // The tiles of the task by number n.  A tile is copied plainly if every key of
-    // it is seen by some query, and taken whole if every key is seen by every
-    // query; both are runs of numbers (tiles of sinks count as neither), as long as
-    // the pages are there.
-    const int tiles = last - first, shift0 = it.tl.head - it.tl.from - first;  // window tile w is number w + shift0
-    const int64_t low = a.window > 0 ? max((int64_t)it.lo - a.window + 1, (int64_t)0) : 0;
-    const int64_t low_all = a.window > 0 ? max((int64_t)it.hi - a.window + 1, (int64_t)0) : 0;
-    const int plain0 = max((int)((low + 63) >> 6) + shift0, max(it.tl.head - first, 0));
-    const int plain1 = min(((it.hi + 1) >> 6) + shift0, tiles);
-    const int whole0 = max((int)((low_all + 63) >> 6) + shift0, plain0);
-    const int whole1 = min(((it.lo + 1) >> 6) + shift0, tiles);
-
-    // where tiles n .. n + 63 are; barriers on both sides
-    const auto read_pages = [&](int n) {
-      sync_lds();
-      if (tid == 0) s_paged = 1;
-      sync_lds();
-      for (int e = tid; e < 512; e += THREADS) {
-        const int t = n + (e >> 3);
-        int64_t at = -1;
-        if (t < tiles) {
-          const int j = (it.tl.at(first + t) << 6) + 8 * (e & 7);
-          if (j <= it.hi && (j + 7 >= low || j < a.sinks)) {
-            const int page = table[j >> a.page_shift];
-            if ((uint32_t)page < (uint32_t)a.num_pages) at = 2 * (page * a.page_stride + (j & in_page) * D);
-            else s_paged = 0;
-          }
-        }
-        s_pages[e] = at;
-      }
-      sync_lds();
-      return __builtin_amdgcn_readfirstlane(s_paged) != 0;
-    };
-    // where this wave's copies of tile i come from: K and V with four waves, one of
-    // them with eight; past the last tile, zeros (so that the loop needs no branch)
-    struct Source {
-      const char *k, *v;
-    };
-    const char* base = reinterpret_cast<const char*>(a.pool + (((int64_t)it.kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0)) + my_off;
-    const int64_t* my_pages = s_pages + (my_key >> 3);
-    const auto plain_source = [&](int64_t at) { return Source{base + at, base + at + (W == 4 ? 2 * a.plane : 0)}; };
-    const auto masked_source = [&](int n, int64_t at, int buf) {
-      bool in = n < tiles && at >= 0;
-      if (in) {
-        const int j = (it.tl.at(first + n) << 6) + my_key;
-        in = j <= it.hi && (j >= low || j < a.sinks);
-      }
-      const unsigned long long there = __ballot(in);
-      if (lane == 0 && wave0 < 4) s_valid[buf][wave0] = every_fourth(there);
-      const char* zero = reinterpret_cast<const char*>(pl.zeros);
-      return Source{in ? base + at : zero, W == 4 && in ? base + at + 2 * a.plane : zero};
-    };
-    const auto copy_block = [&](const Source& x, int buf, int b) {  // b a constant once unrolled
-      const auto go = [&](const char* p, uint32_t dst) {
-        if (b == 0) load_lds16<0, 0>(p, dst);
-        else if (b == 1) load_lds16<64, 4096>(p, dst);
-        else if (b == 2) load_lds16<128, 8192>(p, dst);
-        else load_lds16<192, 12288>(p, dst);
-      };
-      go(x.k, (W == 8 && wave0 >= 4 ? to_v : to_k) + buf * (kTile * 16));
-      if (W == 4) go(x.v, to_v + buf * (kTile * 16));
-    };
-    const auto run_tiles = [&](auto planes, bool careful) {
-    constexpr int NP = decltype(planes)::n;
 #pragma unroll
-    for (int d = 0; d < S; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-    m = -INFINITY;
-    l = 0.0f;
-    if (tid == 0) s_odd = 0;
-    bool paged = read_pages(0), paged_now = paged;  // of the tiles that are copied; that are multiplied
+      for (int x = 0; x < (F32 ? 2 : 1); ++x)
+        qraw[c][x] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(a.q) + (q0 + 16 * c) * (F32 ? 4 : 2) + 16 * x);
+    paged = read_pages(0, fetched);
 #pragma unroll
     for (int t = 0; t < R - 1; ++t) {
       const Source x = masked_source(t, my_pages[t * 8], t);
 #pragma unroll
       for (int b = 0; b < S; ++b) copy_block(x, t, b);
     }
-    int buf = 0;
-    for (int n = 0; n < tiles; ++n, buf = (buf + 1) & (R - 1)) {
-      const int ahead = n + R - 1, after = (buf + R - 1) & (R - 1);  // the tile to copy, where tile n - 1 was
-      // this wave's copies of tile n have landed (those of the next two may be under way), then everybody's
-      loads_done<(R - 2) * kCopies>();
-      sync_lds();
-      if ((ahead & 63) == 0) paged = read_pages(ahead);
-      if ((n & 63) == 0) paged_now = paged;
-      const int64_t at = my_pages[(ahead & 63) * 8];
-      __builtin_amdgcn_sched_barrier(0);
-      const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
-      f32x16 s[2];
-      if (busy) {
-        // all reads of K ahead of its products
-        u32x4 kf[D / 16][2];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c & 1] + (c >> 1) * 256 + t * 128];
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-          for (int n = NQ - 1; n >= 0; --n)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[c][t]), q[c][n], s[t], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      mfma_settle_before_join();
-      const bool whole = paged_now && n >= whole0 && n < whole1;
-      if (careful) {
-        for (int at = tid; at < kTile; at += THREADS) {
-          u32x4 v = s_v[buf * kTile + at];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
-            if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
+  };
+
+  f32x16 o[S];
+  float m, l;
+  bool started = false;
+  for (;;) {
+    if (!started) {
+      if (task < 0) {  // what the other eighths have left
+        __syncthreads();  // every wave has read s_task
+        if (wave0 == 0) {
+          int found = -1;
+          uint64_t open = 0xff;  // a try that fails closes an eighth for good: nine rounds at most
+          for (;;) {
+            const int e = (eighth + lane) & 7;
+            const int left = max(start_of(e + 1) - start_of(e) - kPer, 0);
+            const int taken = __hip_atomic_load(pl.next + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            open &= __ballot(lane < 8 && taken < left);
+            if (open == 0) break;
+            const int at = __ffsll((unsigned long long)open) - 1, f = (eighth + at) & 7;
+            int x = lane == 0 ? atomicAdd(pl.next + f, 1) : 0;
+            x = __builtin_amdgcn_readfirstlane(x);
+            if (x < start_of(f + 1) - start_of(f) - kPer) {
+              found = start_of(f) + kPer + x;
+              break;
+            }
+            open &= ~(1ull << at);
           }
-          s_v[buf * kTile + at] = v;
+          if (lane == 0) s_task = found;
         }
         __syncthreads();
+        task = __builtin_amdgcn_readfirstlane(s_task);
+        if (task < 0) return;
       }
-      Source src;
-      if (paged && ahead >= plain0 && ahead < plain1) src = plain_source(at);
-      else src = masked_source(ahead, at, after);
-      if (!busy) {
+      const PrefillTask* p = pl.tasks + which_task(a, Z, block, task, &kvh);
+      if (tid < 16) reinterpret_cast<int32_t*>(s_tasks + turn)[tid] = reinterpret_cast<const int32_t*>(p)[tid];
+      __syncthreads();
+      start(false);
+    }
+    const int ask = own_left > 0 && tiles >= 3 ? tiles - 3 : 0x3fffffff;
+
+    const auto run_tiles = [&](auto planes, bool careful) {
+      constexpr int NP = decltype(planes)::n;
+      bf16x8 q[D / 16][NQ];
 #pragma unroll
-        for (int b = 0; b < S; ++b) copy_block(src, after, b);
-        continue;
-      }
-      // V of the first two key quarters while the products finish
-      bf16x8 vf[2][S];
-      const auto read_v = [&](int kc) {
+      for (int c = 0; c < D / 16; ++c) query_planes(qraw[c], pl.qmul, q[c]);
 #pragma unroll
-        for (int d = 0; d < S; ++d)
-          vf[kc & 1][d] = join_halves(read_tr(vt, v_at[0] + d * 256 + kc * 64, lane & 1), read_tr(vt, v_at[1] + d * 256 + kc * 64, lane & 1));
-      };
-      read_v(0);
-      read_v(1);
-      __builtin_amdgcn_sched_barrier(0);
-      if (!whole) {
-        const int j0 = it.tl.at(first + n) << 6;
-        uint64_t seen = below(pos - j0 + 1);
-        if (a.window > 0) seen &= ~below((int64_t)pos - a.window + 1 - j0) | below((int64_t)a.sinks - j0);
-        // the first tiles of a task are copied by masks, too
-        if (n < R - 1 || !(paged_now && n >= plain0 && n < plain1)) seen &= *reinterpret_cast<const uint64_t*>(s_valid[buf]);
-        seen >>= 4 * h;
+      for (int d = 0; d < S; ++d)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t w = (uint32_t)(seen >> (32 * t));
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (!(w & (1u << (8 * (r >> 2) + (r & 3))))) s[t][r] = -INFINITY;
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+      m = -INFINITY;
+      l = 0.0f;
+      if (tid == 0) s_odd = 0;
+      bool paged_now = paged;  // of the tiles that are multiplied
+      const int asking = careful ? 0x3fffffff : ask;
+      int event = 0, buf = 0;
+      for (int n = 0; n < tiles; ++n, buf = (buf + 1) & (R - 1)) {
+        const int ahead = n + R - 1, after = (buf + R - 1) & (R - 1);  // the tile to copy, where tile n - 1 was
+        // this wave's copies of tile n have landed (those of the next two may be under way), then everybody's
+        loads_done<(R - 2) * kCopies>();
+        sync_lds();
+        if (n == event) {  // one branch for all that most tiles have not
+          if ((ahead & 63) == 0) paged = read_pages(ahead, false);
+          if ((n & 63) == 0) paged_now = paged;
+          if (n >= asking) {
+            // the next task: its number, two tiles later its description, at the
+            // end of the last tile its page entries
+            if (n == ask) {
+              if (wave0 == 0) {
+                const int x = __builtin_amdgcn_readfirstlane(lane == 0 ? atomicAdd(pl.next + eighth, 1) : 0);
+                if (lane == 0) s_task = x < own_left ? own + x : -1;
+                if (x < own_left) {
+                  int head;
+                  const PrefillTask* p = pl.tasks + which_task(a, Z, block, own + x, &head);
+                  if (lane == 0) s_head = head;
+                  if (lane < 16) load_lds4(reinterpret_cast<const int32_t*>(p) + lane, lds_offset(s_tasks + (turn ^ 1)));
+                }
+              }
+            } else if (n == ask + 2 && __builtin_amdgcn_readfirstlane(s_task) >= 0) {
+              const PrefillTask t = read_task(s_tasks[turn ^ 1]);
+              const int t_low = in_window(t.lo);
+              for (int e = wave0 * 64; e < 512; e += THREADS) {
+                const int i = (e + lane) >> 3, j = key_in(t.k0, t.head, t.from, i) + 8 * (lane & 7);
+                const bool any = i < t.k1 - t.k0 && any_sees(j, t.hi, t_low);
+                load_lds4(a.table + (int64_t)t.row * a.width + (any ? j >> a.page_shift : 0), lds_offset(s_entry) + e * 4);
+              }
+            }
+          }
+          // the next of: ahead and n at multiples of 64, the last three tiles
+          event = min(min(((ahead + 64) & ~63) - (R - 1), (n + 64) & ~63), max(asking, n + 1));
         }
-      }
-      float tops[2] = {s[0][0], s[1][0]};
+        const int64_t at = my_pages[(ahead & 63) * 8];
+        __builtin_amdgcn_sched_barrier(0);
+        const u32x4 *kt = s_k + buf * kTile, *vt = s_v + buf * kTile;
+        f32x16 s[2];
+        if (busy) {
+          // all reads of K ahead of its products
+          u32x4 kf[D / 16][2];
 #pragma unroll
-      for (int r = 1; r < 16; ++r)
+          for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) tops[t] = fmaxf(tops[t], s[t][r]);
-      const float top = max_halves(fmaxf(tops[0], tops[1])) * pl.c;
-      // the reference follows only when it is left far behind: weights up to 2^8
-      // are as exact, and rescaling costs a pass over o
-      if (__any(top > m + 8.0f)) {
-        const float mn = fmaxf(m, top);
-        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
-        m = mn;
-        l *= f;
+            for (int t = 0; t < 2; ++t) kf[c][t] = kt[k_at[c & 1] + (c >> 1) * 256 + t * 128];
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int d = 0; d < S; ++d) o[d] *= f;
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      bf16x8 w[2][NP];
-      const auto weights = [&](int kc) {
-        float p[8];
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(fmaf(s[kc >> 1][8 * (kc & 1) + e], pl.c, -ref));
-          if (NP > 1) l += p[e];
+            for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int n = NQ - 1; n >= 0; --n)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[c][t]), q[c][n], s[t], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        split_weights<NP>(p, w[kc & 1]);
-        if (NP == 1) {  // the sum of the rounded weights: what rounding does to all of them alike cancels
-          typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-          const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+        mfma_settle_before_join();
+        const bool whole = paged_now && n >= whole0 && n < whole1;
+        if (careful) {
+          for (int at = tid; at < kTile; at += THREADS) {
+            u32x4 v = s_v[buf * kTile + at];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{w[kc & 1][0][2 * e], w[kc & 1][0][2 * e + 1]}, one, l, false);
+            for (int e = 0; e < 4; ++e) {
+              if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
+              if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
+            }
+            s_v[buf * kTile + at] = v;
+          }
+          __syncthreads();
         }
-      };
-      weights(0);
-      __builtin_amdgcn_sched_barrier(0);
-      // the next quarter's weights are formed beside this one's products, and
-      // the copies of the tile ahead spread between them
+        Source src;
+        if (paged && ahead >= plain0 && ahead < plain1) src = plain_source(at);
+        else src = masked_source(ahead, at, after);
+        if (!busy) {
 #pragma unroll
-      for (int kc = 0; kc < 4; ++kc) {
-        if (kc < S) copy_block(src, after, kc);
-        if (kc < 3) weights(kc + 1);
+          for (int b = 0; b < S; ++b) copy_block(src, after, b);
+          continue;
+        }
+        // V of the first two key quarters while the products finish
+        bf16x8 vf[2][S];
+        const auto read_v = [&](int kc) {
 #pragma unroll
-        for (int d = 0; d < S; ++d)
+          for (int d = 0; d < S; ++d)
+            vf[kc & 1][d] = join_halves(read_tr(vt, v_at[0] + d * 256 + kc * 64, lane & 1), read_tr(vt, v_at[1] + d * 256 + kc * 64, lane & 1));
+        };
+        read_v(0);
+        read_v(1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!whole) {
+          const int j0 = key_of(n);
+          uint64_t seen = below(pos - j0 + 1);
+          if (a.window > 0) seen &= ~below((int64_t)pos - a.window + 1 - j0) | below((int64_t)a.sinks - j0);
+          // the first tiles of a task are copied by masks, too
+          if (n < R - 1 || !(paged_now && n >= plain0 && n < plain1)) seen &= *reinterpret_cast<const uint64_t*>(s_valid[buf]);
+          seen >>= 4 * h;
 #pragma unroll
-          for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[kc & 1][d], w[kc & 1][n], o[d], 0, 0, 0);
-        if (kc < 2) read_v(kc + 2);
-        if (NP == 1 && kc < 3) {
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t w = (uint32_t)(seen >> (32 * t));
 #pragma unroll
-          for (int d = 0; d < S; ++d) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a product,
-            __builtin_amdgcn_sched_group_barrier(0x402, 7, 0);  // its share of the vector work
+            for (int r = 0; r < 16; ++r)
+              if (!(w & (1u << (8 * (r >> 2) + (r & 3))))) s[t][r] = -INFINITY;
           }
         }
+        float tops[2] = {s[0][0], s[1][0]};
+#pragma unroll
+        for (int r = 1; r < 16; ++r)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) tops[t] = fmaxf(tops[t], s[t][r]);
+        const float top = max_halves(fmaxf(tops[0], tops[1])) * pl.c;
+        // the reference follows only when it is left far behind: weights up to 2^8
+        // are as exact, and rescaling costs a pass over o
+        if (__any(top > m + 8.0f)) {
+          const float mn = fmaxf(m, top);
+          const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int d = 0; d < S; ++d) o[d] *= f;
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        bf16x8 w[2][NP];
+        const auto weights = [&](int kc) {
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[kc >> 1][8 * (kc & 1) + e], pl.c, -ref));
+            if (NP > 1) l += p[e];
+          }
+          split_weights<NP>(p, w[kc & 1]);
+          if (NP == 1) {  // the sum of the rounded weights: what rounding does to all of them alike cancels
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{w[kc & 1][0][2 * e], w[kc & 1][0][2 * e + 1]}, one, l, false);
+          }
+        };
+        weights(0);
         __builtin_amdgcn_sched_barrier(0);
+        // the next quarter's weights are formed beside this one's products, and
+        // the copies of the tile ahead spread between them
+#pragma unroll
+        for (int kc = 0; kc < 4; ++kc) {
+          if (kc < S) copy_block(src, after, kc);
+          if (kc < 3) weights(kc + 1);
+#pragma unroll
+          for (int d = 0; d < S; ++d)
+#pragma unroll
+            for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[kc & 1][d], w[kc & 1][n], o[d], 0, 0, 0);
+          if (kc < 2) read_v(kc + 2);
+          if (NP == 1 && kc < 3) {
+#pragma unroll
+            for (int d = 0; d < S; ++d) {
+              __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a product,
+              __builtin_amdgcn_sched_group_barrier(0x402, 7, 0);  // its share of the vector work
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-    }
-    mfma_settle_before_join();
-    loads_done<0>();
+      mfma_settle_before_join();
+      loads_done<0>();
     };
     // A weight of 0 does not keep out a value that is infinite or NaN.  Where a
     // result is not finite, the task is run once more with such values taken out
     // of the tiles; then they are added for the queries that see them.
-    for (bool careful = false;; careful = true) {
+    bool careful = false;
+    for (;;) {
       if constexpr (F32) run_tiles(Planes<3>(), careful);
       else if (few) run_tiles(Planes<2>(), careful);
       else run_tiles(Planes<1>(), careful);
@@ -530,24 +592,32 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       for (int d = 0; d < S; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) odd |= !(fabsf(o[d][r]) < INFINITY);
-      if (tid == 0) s_task = next_task;
       if (!careful && odd) s_odd = 1;
-      __syncthreads();  // also: the next tiles go over buffers that may still be read
-      const bool again = s_odd != 0 && !careful;
-      __syncthreads();
-      if (!again) {
-        odd_task = careful;
-        break;
+      if (!careful && tiles < 3 && tid == 0) {  // too short to ask ahead
+        const int x = own_left > 0 ? atomicAdd(pl.next + eighth, 1) : 0;
+        s_task = x < own_left ? own + x : -1;
       }
+      __syncthreads();  // also: the next tiles go over buffers that may still be read
+      if (careful || s_odd == 0) break;
+      careful = true;
+      start(false);
     }
-    task = __builtin_amdgcn_readfirstlane(s_task);
-    if (odd_task) {
-      for (int j = it.tl.at(first) << 6; j <= it.hi; ++j) {
-        const int tile = j >> 6, i = tile < it.tl.head ? tile : tile - it.tl.from + it.tl.head;
-        if ((tile >= it.tl.head && tile < it.tl.from) || i < first || i >= last) continue;
-        const int page = table[j >> a.page_shift];
+    const PrefillTask done = read_task(s_tasks[turn]);
+    const int done_head = kvh;
+    task = own_left > 0 ? __builtin_amdgcn_readfirstlane(s_task) : -1;
+    started = task >= 0 && ask < 0x3fffffff;
+    turn ^= 1;
+    if (started) {
+      kvh = __builtin_amdgcn_readfirstlane(s_head);
+      start(true);
+    }
+    if (careful) {
+      for (int j = key_in(done.k0, done.head, done.from, 0); j <= done.hi; ++j) {
+        const int tile = j >> 6, i = tile < done.head ? tile : tile - done.from + done.head;
+        if ((tile >= done.head && tile < done.from) || i < done.k0 || i >= done.k1) continue;
+        const int page = a.table[(int64_t)done.row * a.width + (j >> a.page_shift)];
         if ((uint32_t)page >= (uint32_t)a.num_pages || !sees(a, pos, j)) continue;
-        const uint16_t* v = a.pool + a.plane + page * a.page_stride + (((int64_t)it.kvh << a.page_shift) + (j & in_page)) * D + 4 * h;
+        const uint16_t* v = a.pool + a.plane + page * a.page_stride + (((int64_t)done_head << a.page_shift) + (j & in_page)) * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < S; ++d)
 #pragma unroll
@@ -563,10 +633,11 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       }
     }
     l += __shfl_xor(l, 32, 64);
-    if (it.parts == 1) {
+    const Row mine = row_of(done, done_head);
+    if (done.parts == 1) {
       const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-      if (has) {
-        const int64_t at = (int64_t)(it.first + qi) * a.ldo + (int64_t)hq * D + 4 * h;
+      if (mine.has) {
+        const int64_t at = (int64_t)(done.first + mine.qi) * a.ldo + (int64_t)mine.hq * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < S; ++d)
 #pragma unroll
@@ -579,8 +650,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
           }
       }
     } else if (busy) {
-      const int64_t slot = it.slot + it.part;
-      if (tid == 0) pl.records[slot] = JoinRecord{it.part == 0 ? it.parts : 0, it.row, it.kvh, it.tile};
+      const int64_t slot = (int64_t)done_head * pl.head[1] + done.slot + done.part;
+      if (tid == 0) pl.records[slot] = JoinRecord{done.part == 0 ? done.parts : 0, done.row, done_head, done.tile};
       const int r0 = wave * 32 + n32;
       float* dst = pl.part + (slot * ROWS + r0) * D + 4 * h;
 #pragma unroll
@@ -602,7 +673,7 @@ template <int D, int ROWS>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ int s_list[kPrefillSlots];
   const int wave = threadIdx.x >> 6, waves = gridDim.x * 4, me = blockIdx.x * 4 + wave;
-  const int n = split_items(pl.records, pl.row_slot[a.rows], s_list);
+  const int n = split_items(pl.records, pl.head[1] * a.heads, s_list);
   for (int x = me; x < n * ROWS; x += waves) {
     const int slot = s_list[x / ROWS], r = x % ROWS;
     const JoinRecord rec = pl.records[slot];

@@ -306,6 +306,19 @@ def test_queries_past_the_last_row_are_left_alone(lq):
     assert torch.equal(got[:15], want) and (got[15:] == 7).all()
 
 
+def test_prefix_that_does_not_ascend_stays_inside(lq):
+    """Not a valid call, but no address depends on cu: nothing outside out and the workspace is written."""
+    c = Case([900] * 40, 1, 1, 64, 16, news=[10] * 40)
+    need = kv.loopq_attn_workspace_bytes(400, 1, 40, 64)
+    big = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    cu = i32([0, 400] * 20 + [0])
+    out = torch.full((500, 1, 64), 7.0, dtype=c.q.dtype, device="cuda")
+    kv.loopq_attn_prefill(c.pool, c.slab, c.t, cu, c.q, out[:400], big[:need], c.scale)
+    kv.loopq_attn_prefill(c.pool, c.slab, c.t, i32([-5, 2 ** 31 - 1, -2 ** 31] * 13 + [0, 9]), c.q, out[:400], big[:need], c.scale)
+    torch.cuda.synchronize()
+    assert (big[need:] == 77).all() and (out[400:] == 7).all()
+
+
 @BOTH
 @pytest.mark.parametrize("news", [None, [300, 64, 1]])
 def test_same_bits_every_time_and_on_another_stream(lq, news, dtype):
