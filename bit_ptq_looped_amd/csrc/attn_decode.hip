@@ -51,12 +51,13 @@ __device__ __forceinline__ int64_t decode_piece(int64_t total) {
 
 // Tiles first .. last - 1 (at least one) of a query tile's keys, by one wave: O^T
 // in registers (lane: head lane % 16, columns 16 d + 4 (lane / 16) + r), the
-// reference m and l = the sum of the weights.  `tile` is the wave's own LDS.  K
-// goes from memory to the product's operand, V through LDS to be transposed; the
-// next tile's loads are issued before this one's weights are formed.
+// reference m and l = the sum of the weights.  `tile` and `rows` are the wave's own
+// LDS.  K goes from memory to the product's operand, V through LDS to be
+// transposed; the next tile's loads are issued before this one's weights are
+// formed.
 template <int D, bool F32>
 __device__ __forceinline__ void decode_tiles(const AttnArgs& a, const AttnPlan& pl, int row, int kvh, int hq, bool has, int pos,
-                                             const Tiles& tl, int first, int last, u32x4* tile, f32x4 (&o)[D / 16],
+                                             const Tiles& tl, int first, int last, u32x4* tile, const char** rows, f32x4 (&o)[D / 16],
                                              float& m, float& l) {
   constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
   constexpr int C = D / 8;                  // chunks of a row
@@ -83,25 +84,26 @@ __device__ __forceinline__ void decode_tiles(const AttnArgs& a, const AttnPlan& 
     return page;  // as it stands in the table: the load is not waited for here
   };
   const auto real = [&](int page) { return (uint32_t)page < (uint32_t)a.num_pages ? page : -1; };
+  // Where the keys' rows start goes through LDS: a load needs one address from
+  // there and an offset.  A hidden key reads the pool's first row instead.
+  const char* const pool = reinterpret_cast<const char*>(a.pool);
   u32x4 kr[2][D / 32], vr[NV];
   const auto load_tile = [&](int i, int page) {
-    const int j0 = tl.at(i) << 5;
-    const int in_page = (1 << a.page_shift) - 1;
+    const int in_page = ((tl.at(i) << 5) + lane) & ((1 << a.page_shift) - 1);
+    if (lane < kDecodeKeys)
+      rows[lane] = page < 0 ? pool : pool + 2 * (page * a.page_stride + (((int64_t)kvh << a.page_shift) + in_page) * D);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int key = 16 * t + n16, pg = __shfl(page, key, 64);
-      const uint16_t* p = a.pool + pg * a.page_stride + (((int64_t)kvh << a.page_shift) + ((j0 + key) & in_page)) * D + 8 * g;
-      if (pg >= 0)
+      const char* p = rows[16 * t + n16] + 16 * g;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) kr[t][c] = *reinterpret_cast<const u32x4*>(p + 32 * c);
+      for (int c = 0; c < D / 32; ++c) kr[t][c] = *reinterpret_cast<const u32x4*>(p + 64 * c);
     }
 #pragma unroll
     for (int x = 0; x < NV; ++x) {
-      const int at = lane + 64 * x, key = at / C, ch = at - key * C, pg = __shfl(page, key, 64);
-      const uint16_t* p = a.pool + a.plane + pg * a.page_stride +
-                          (((int64_t)kvh << a.page_shift) + ((j0 + key) & in_page)) * D + 8 * ch;
-      vr[x] = u32x4{0, 0, 0, 0};  // a hidden key's values count for nothing, whatever they hold
-      if (pg >= 0) vr[x] = *reinterpret_cast<const u32x4*>(p);
+      const int at = lane + 64 * x, key = at / C, ch = at - key * C;
+      vr[x] = *reinterpret_cast<const u32x4*>(rows[key] + 2 * a.plane + 16 * ch);
     }
   };
 
@@ -122,6 +124,12 @@ __device__ __forceinline__ void decode_tiles(const AttnArgs& a, const AttnPlan& 
           s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kr[t][c]), q[c][n], s[t], 0, 0, 0);
     }
     // V to LDS, then the next tile's loads
+    const uint32_t now = seen;
+    if (now != 0xffffffffu) {  // a hidden key's values count for nothing, whatever was read
+#pragma unroll
+      for (int x = 0; x < NV; ++x)
+        if (!((now >> ((lane + 64 * x) / C)) & 1)) vr[x] = u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int x = 0; x < NV; ++x) {
       const int at = lane + 64 * x, key = at / C, ch = at - key * C;
@@ -130,7 +138,6 @@ __device__ __forceinline__ void decode_tiles(const AttnArgs& a, const AttnPlan& 
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     mfma_settle_before_join();
-    const uint32_t now = seen;
     if (i + 1 < last) {
       page = real(page);
       seen = (uint32_t)__ballot(page >= 0);
@@ -198,8 +205,9 @@ __device__ __forceinline__ void store_columns(const AttnArgs& a, int64_t at, con
 template <int D, bool F32>
 __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ u32x4 s_v[4][kDecodeKeys * D / 8];
+  __shared__ const char* s_rows[4][kDecodeKeys];
   extern __shared__ int64_t s_prefix[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, g = lane >> 4;
   const int gts = (a.group + kDecodeRows - 1) / kDecodeRows, items = a.heads * gts;
   decode_prefix(a, items, s_prefix);
@@ -223,7 +231,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPla
     const int hq = kvh * a.group + head;
     f32x4 o[D / 16];
     float m, l;
-    decode_tiles<D, F32>(a, pl, row, kvh, hq, has, pos, tl, first, last, tile, o, m, l);
+    decode_tiles<D, F32>(a, pl, row, kvh, hq, has, pos, tl, first, last, tile, s_rows[wave], o, m, l);
     if (first == 0 && last == tl.n) {
       if (has) store_columns<D>(a, row * a.ldo + (int64_t)hq * D + 4 * g, o, l);
     } else if (has) {
@@ -256,8 +264,9 @@ constexpr int kShortWaves = 8;
 template <int D, bool F32>
 __global__ __launch_bounds__(64 * kShortWaves, 2) void decode_short_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ u32x4 s_v[kShortWaves][kDecodeKeys * D / 8];  // a wave's V tile, then its O: [16][D] floats, as many bytes
+  __shared__ const char* s_rows[kShortWaves][kDecodeKeys];
   __shared__ float s_m[kShortWaves][kDecodeRows], s_l[kShortWaves][kDecodeRows];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g = lane >> 4;
   const int gts = (a.group + kDecodeRows - 1) / kDecodeRows, items = a.heads * gts;
   const int row = blockIdx.x / items, item = blockIdx.x - row * items;
   const int kvh = item / gts, gt = item - kvh * gts, head = gt * kDecodeRows + n16, hq = kvh * a.group + head;
@@ -268,7 +277,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void decode_short_kernel(AttnA
   float m = -INFINITY, l = 0.0f;
   if (first < last) {
     f32x4 o[D / 16];
-    decode_tiles<D, F32>(a, pl, row, kvh, hq, has, pos, tl, first, last, s_v[wave], o, m, l);
+    decode_tiles<D, F32>(a, pl, row, kvh, hq, has, pos, tl, first, last, s_v[wave], s_rows[wave], o, m, l);
     float* so = reinterpret_cast<float*>(s_v[wave]) + n16 * D + 4 * g;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4*>(so + 16 * d) = o[d];
