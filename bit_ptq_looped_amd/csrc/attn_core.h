@@ -28,7 +28,7 @@ constexpr int kPrefillKeys = 64;
 // A split item: how many parts it has and which.  One record per decode piece
 // (of the item whose first part is the piece's last) or per prefill slot (of
 // the item whose first part took it); parts is 0 where there is none.
-struct JoinRecord {
+struct __attribute__((aligned(16))) JoinRecord {
   int32_t parts, row, item, tile;
 };
 
@@ -209,10 +209,25 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t at, const f
 }
 
 // Parts first, first + step, ... of n of one row, one wave: columns lane and
-// lane + 64 of the sum at the reference m of all n parts, and l.
+// lane + 64 of the sum at the reference m of all n parts, and l.  Bound by trips
+// to memory (the parts come from other XCDs), so that the first eight parts are on
+// their way before m is known.
 template <int D, int ROWS, class F>
 __device__ __forceinline__ float join_parts(const AttnPlan& pl, int n, int first, int step, int r, F slot_of, float (&o)[2]) {
   const int lane = threadIdx.x & 63;
+  float p[8][2], pm[8], psum[8];
+  const auto load = [&](int i0) {  // no branches, so that all are one trip
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int64_t slot = slot_of(min(i0 + x * step, n - 1));
+      const float* at = pl.part + (slot * ROWS + r) * D;
+      pm[x] = pl.ml[slot * 2 * ROWS + r];
+      psum[x] = pl.ml[(slot * 2 + 1) * ROWS + r];
+      p[x][0] = at[lane];
+      if (D > 64) p[x][1] = at[min(lane + 64, D - 1)];
+    }
+  };
+  load(first);
   float m = -INFINITY;
   for (int i = lane; i < n; i += 64) m = fmaxf(m, pl.ml[slot_of(i) * 2 * ROWS + r]);
 #pragma unroll
@@ -220,36 +235,51 @@ __device__ __forceinline__ float join_parts(const AttnPlan& pl, int n, int first
   const float ref = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
   o[0] = o[1] = 0.0f;
-#pragma unroll 8
-  for (int i = first; i < n; i += step) {
-    const int64_t slot = slot_of(i);
-    const float f = __builtin_amdgcn_exp2f(pl.ml[slot * 2 * ROWS + r] - ref);
-    const float* p = pl.part + (slot * ROWS + r) * D;
-    l = fmaf(f, pl.ml[(slot * 2 + 1) * ROWS + r], l);
-    o[0] = fmaf(f, p[lane], o[0]);
-    if (D > 64) o[1] = fmaf(f, lane + 64 < D ? p[lane + 64] : 0.0f, o[1]);
+  for (int i0 = first; i0 < n; i0 += 8 * step) {
+    if (i0 != first) load(i0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const bool in = i0 + x * step < n;  // the last part stands in for those past it
+      const float f = __builtin_amdgcn_exp2f(pm[x] - ref);
+      l = in ? fmaf(f, psum[x], l) : l;
+      o[0] = in ? fmaf(f, p[x][0], o[0]) : o[0];
+      if (D > 64) o[1] = in ? fmaf(f, p[x][1], o[1]) : o[1];
+    }
   }
   return l;
 }
 
 // The records among n that stand for an item, into `list` in their order (the
-// same in every work-group); their number.  256 threads, ends with a barrier.
-__device__ __forceinline__ int split_items(const JoinRecord* records, int n, int* list) {
-  __shared__ int count[4];
+// same in every work-group), with their place; their number.  256 threads, 2048
+// records at a time so that they are one trip to memory; ends with a barrier.
+struct SplitItem {
+  int32_t parts, row, item, tile, at;
+};
+__device__ __forceinline__ int split_items(const JoinRecord* records, int n, SplitItem* list) {
+  __shared__ int count[32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int base = 0;
-  for (int i0 = 0; i0 < n; i0 += 256) {
-    const int i = i0 + tid;
-    const uint64_t is = __ballot(i < n && records[i].parts > 0);
-    if (lane == 0) count[wave] = __popcll(is);
-    __syncthreads();
-    int at = base;
+  for (int i0 = 0; i0 < n; i0 += 2048) {
+    JoinRecord rec[8];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      at += w < wave ? count[w] : 0;
-      base += count[w];
+    for (int c = 0; c < 8; ++c) {
+      const int i = i0 + 256 * c + tid;
+      rec[c] = i < n ? records[i] : JoinRecord{0, 0, 0, 0};
     }
-    if ((is >> lane) & 1) list[at + __popcll(is & ((1ull << lane) - 1))] = i;
+    uint64_t is[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      is[c] = __ballot(rec[c].parts > 0);
+      if (lane == 0) count[4 * c + wave] = __popcll(is[c]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      for (int w = 0; w < 4; ++w) {
+        if (w == wave && ((is[c] >> lane) & 1))
+          list[base + __popcll(is[c] & ((1ull << lane) - 1))] = SplitItem{rec[c].parts, rec[c].row, rec[c].item, rec[c].tile, i0 + 256 * c + tid};
+        base += count[4 * c + w];
+      }
     __syncthreads();
   }
   return base;

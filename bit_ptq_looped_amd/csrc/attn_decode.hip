@@ -313,14 +313,14 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void decode_short_kernel(AttnA
 // of the parts each, added in the order of the waves.
 template <int D>
 __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a, AttnPlan pl) {
-  __shared__ int s_list[kDecodePieces];
+  __shared__ SplitItem s_list[kDecodePieces];
   __shared__ float s_o[4][2][64], s_l[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int gts = (a.group + kDecodeRows - 1) / kDecodeRows, heads = min(kDecodeRows, a.group);
   const int n = split_items(pl.records, kDecodePieces, s_list);
   for (int x = blockIdx.x; x < n * heads; x += gridDim.x) {
-    const int w0 = s_list[x / heads], r = x % heads;
-    const JoinRecord rec = pl.records[w0];
+    const SplitItem rec = s_list[x / heads];
+    const int w0 = rec.at, r = x % heads;
     const int kvh = rec.item / gts, gt = rec.item - kvh * gts;
     if (r >= a.group - gt * kDecodeRows) continue;
     float o[2];

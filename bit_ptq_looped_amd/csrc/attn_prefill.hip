@@ -671,12 +671,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
 // tile belongs to.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan pl) {
-  __shared__ int s_list[kPrefillSlots];
+  __shared__ SplitItem s_list[kPrefillSlots];
   const int wave = threadIdx.x >> 6, waves = gridDim.x * 4, me = blockIdx.x * 4 + wave;
   const int n = split_items(pl.records, pl.head[1] * a.heads, s_list);
   for (int x = me; x < n * ROWS; x += waves) {
-    const int slot = s_list[x / ROWS], r = x % ROWS;
-    const JoinRecord rec = pl.records[slot];
+    const SplitItem rec = s_list[x / ROWS];
+    const int slot = rec.at, r = x % ROWS;
     int first;
     const int64_t rows = (int64_t)row_queries(a, rec.row, &first) * a.group, rr = (int64_t)rec.tile * ROWS + r;
     if (rr >= rows) continue;
