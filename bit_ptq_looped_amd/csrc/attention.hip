@@ -17,13 +17,21 @@
 // products with the bf16 keys and values are exact; bf16 queries are exact
 // alone.
 //
+// fp32 queries and weights are cut, not rounded, into their planes, and no plane of
+// a weight is 0 unless the weight is, so that an infinite key or value meets every
+// plane as in the formula.  bf16 queries: weights go to the product as one bf16
+// plane (rounded by up to 2^-8 of themselves, and l sums the rounded weights, so that
+// what rounding does to all alike cancels), as two where few keys share the sum
+// and in decode, where the product costs nothing beside the bytes.
+//
 // Work is cut by length, not by row: the visible key tiles of all (row, key
-// head, query tile) items form one line, cut into equal pieces, one per wave
-// (decode) or work-group (prefill).  Lengths are read on the device, so ragged
-// rows balance and the launch shape never depends on them.  An item that lies
-// in one piece is finished there; the others leave (m, l, O) per piece, at most
-// two a piece, and a second launch joins them in the order of the keys: the
-// result depends on the inputs alone.
+// head, query tile) items form one line, shared out evenly.  Decode cuts it into
+// equal pieces, one per wave; prefill keeps items whole as tasks that work-groups
+// take in turn, and splits those longer than a work-group's even share.  Lengths
+// are read on the device, so ragged rows balance and the launch shape never
+// depends on them.  An item that lies in one piece is finished there; the others
+// leave (m, l, O) per piece, and a last launch joins them in the order of the keys:
+// the result depends on the inputs alone.
 #include "attn_core.h"
 
 namespace loopq {

@@ -124,6 +124,10 @@ __device__ __forceinline__ int find(const T* p, int n, T u) {
 // where nothing is left): all planes times an infinite key are that infinity.
 template <int N>
 __device__ __forceinline__ void query_planes(const u32x4 (&raw)[N == 1 ? 1 : 2], float mul, bf16x8 (&q)[N]) {
+  if (N == 1 && mul == 1.0f) {
+    q[0] = __builtin_bit_cast(bf16x8, raw[0]);
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float x = mul * (N == 1 ? bf16_bits_to_float(e & 1 ? raw[0][e >> 1] >> 16 : raw[0][e >> 1] & 0xffffu) : __uint_as_float(raw[N > 1 ? e >> 2 : 0][e & 3]));
@@ -273,13 +277,19 @@ __device__ __forceinline__ int split_items(const JoinRecord* records, int n, Spl
       if (lane == 0) count[4 * c + wave] = __popcll(is[c]);
     }
     __syncthreads();
+    const int mine = lane < 32 ? count[lane] : 0;
+    int upto = mine;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      for (int w = 0; w < 4; ++w) {
-        if (w == wave && ((is[c] >> lane) & 1))
-          list[base + __popcll(is[c] & ((1ull << lane) - 1))] = SplitItem{rec[c].parts, rec[c].row, rec[c].item, rec[c].tile, i0 + 256 * c + tid};
-        base += count[4 * c + w];
-      }
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += y;
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int at = base + __shfl(upto - mine, 4 * c + wave, 64) + __popcll(is[c] & ((1ull << lane) - 1));
+      if ((is[c] >> lane) & 1) list[at] = SplitItem{rec[c].parts, rec[c].row, rec[c].item, rec[c].tile, i0 + 256 * c + tid};
+    }
+    base += __shfl(upto, 31, 64);
     __syncthreads();
   }
   return base;

@@ -1,5 +1,13 @@
 // Attention of one new token per row over the paged cache (attention.hip has
 // the method).
+//
+// Bound by the bytes of K and V, each read once: a tile of 32 keys is 16 KB at
+// D = 128, and a wave keeps the next one in flight in registers while it works on
+// one, 2048 waves of them (32 MB) over the chip.  48 rows of up to 8192 tokens, 20
+// heads of 128, bf16: 2.08 GB in 367 us, 5.7 TB/s; 3 rows of 131071 tokens, 4 key
+// heads for 32 query heads, fp32 queries: 0.81 GB in 170 us, 4.7 TB/s (212 us while the
+// three planes of the queries spilled registers in the loop: a reload waits for the
+// loads before it).
 #include "attn_core.h"
 
 namespace loopq {
@@ -202,6 +210,8 @@ __device__ __forceinline__ void store_columns(const AttnArgs& a, int64_t at, con
   }
 }
 
+// A piece of the line of tiles per wave: 2048 pieces are two work-groups for each
+// CU, as many as the registers hold.
 template <int D, bool F32>
 __global__ __launch_bounds__(256, 2) void decode_attn_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ u32x4 s_v[4][kDecodeKeys * D / 8];
@@ -310,7 +320,9 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void decode_short_kernel(AttnA
 }
 
 // Joins split items: one work-group per (item, head), its four waves a quarter
-// of the parts each, added in the order of the waves.
+// of the parts each, added in the order of the waves.  Trips to memory: the
+// records, then m and the first parts, then eight parts a wave at a time; 9 us for
+// 960 items of two or three parts, 11 us for 12 items of 170 (4 us with nothing to do).
 template <int D>
 __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ SplitItem s_list[kDecodePieces];

@@ -1,5 +1,15 @@
 // Attention of several new tokens a row over the paged cache, causal, with a
 // sliding window and sinks (attention.hip has the method).
+//
+// Bound by arithmetic where prompts are long: 2 prompts of 8192 tokens, 16 heads of
+// 128, bf16: 0.55 TFLOP in 560 us, 980 TFLOP/s (a large bf16 matrix product
+// reaches 1263 here); the shader clock reads 1.7 GHz meanwhile, so that what counts is
+// work per key tile, 2.1 us for 256 rows.  Steps on the way: products of 128 rows
+// from K and V through registers 1438 us; copied to LDS without registers 887; the
+// reference moved only when left behind, reads ahead of the products, tasks by XCD
+// 655; 256 rows, a ring of buffers, heads in blocks 608; tiles without masks and
+// checks as runs of numbers 561.  Without effect: three buffers instead of four,
+// barriers split in two, wave priorities, other mixes of products and vector work.
 #include "attn_core.h"
 
 namespace loopq {
@@ -188,9 +198,11 @@ __device__ __forceinline__ void sync_lds() {
 
 // A work-group takes a task after another: W waves of 32 rows each over tiles of
 // 64 keys, K and V of the next three tiles on their way to a ring of four
-// buffers in LDS while one is multiplied.  The next task is asked for, and its
-// description and page entries fetched, during the last three tiles, and its first
-// tiles are on their way while results are stored.  Keys that no query of the item
+// buffers in LDS while one is multiplied.  The next task is asked for late, so
+// that no work-group keeps one waiting while another is idle, its description and
+// page entries are fetched during the last three tiles, and its first tiles are on
+// their way while results are stored (12 rows with 1500 new tokens, 32 query heads of
+// 96, window 1000: asked for at the start 209 us, late 190, fetched ahead 180).  Keys that no query of the item
 // sees are read from a line of zeros.  fp32 queries hold three planes in registers
 // and take half the rows.
 template <int D, bool F32, int W>
@@ -252,7 +264,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   bool paged;        // of the tiles that are copied
   bool few, busy;    // few keys a query; the wave has rows
   int pos;           // of this lane's query
-  u32x4 qraw[D / 16][F32 ? 2 : 1];
+  int64_t q0;        // where this lane's part of its query starts
 
   const auto key_in = [&](int k0, int head, int from, int n) {  // first key of tile n of a task
     const int i = k0 + n;
@@ -314,16 +326,19 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     int qi, hq, pos;
   };
   const auto row_of = [&](const PrefillTask& t, int kvh) {
-    const int64_t rows = (int64_t)t.n * a.group, rr = (int64_t)t.tile * ROWS + wave * 32 + n32;
-    const int64_t rq = min(rr, rows - 1);
+    const int q = t.lo - (t.len - t.n);  // the tile's first query
+    const int64_t before = (int64_t)t.tile * ROWS;
+    const int g0 = (int)(before - (int64_t)q * a.group);  // and the head of its first row
+    const int left = (int)min((int64_t)t.n * a.group - before, (int64_t)ROWS), x = wave0 * 32 + n32;
+    const uint32_t u = g0 + min(x, left - 1), dq = u / (uint32_t)a.group;
     Row r;
-    r.has = rr < rows;
-    r.qi = (int)(rq / a.group);
-    r.hq = kvh * a.group + (int)(rq - (int64_t)r.qi * a.group);
+    r.has = x < left;
+    r.qi = q + (int)dq;
+    r.hq = kvh * a.group + (int)(u - dq * a.group);
     r.pos = t.len - t.n + r.qi;
     return r;
   };
-  // queries and first tiles of `it` on their way; no copy may be under way
+  // the task's first tiles on their way; no copy may be under way
   const auto start = [&](bool fetched) {
     const PrefillTask t = read_task(s_tasks[turn]);
     tiles = t.k1 - t.k0;
@@ -344,12 +359,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     const Row r = row_of(t, kvh);
     pos = r.pos;
     busy = (int64_t)t.tile * ROWS + wave0 * 32 < (int64_t)t.n * a.group;
-    const int64_t q0 = (int64_t)(t.first + r.qi) * a.ldq + (int64_t)r.hq * D + 8 * h;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-      for (int x = 0; x < (F32 ? 2 : 1); ++x)
-        qraw[c][x] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(a.q) + (q0 + 16 * c) * (F32 ? 4 : 2) + 16 * x);
+    q0 = (int64_t)(t.first + r.qi) * a.ldq + (int64_t)r.hq * D + 8 * h;
     paged = read_pages(0, fetched);
 #pragma unroll
     for (int t = 0; t < R - 1; ++t) {
@@ -391,7 +401,9 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
         if (task < 0) return;
       }
       const PrefillTask* p = pl.tasks + which_task(a, Z, block, task, &kvh);
-      if (tid < 16) reinterpret_cast<int32_t*>(s_tasks + turn)[tid] = reinterpret_cast<const int32_t*>(p)[tid];
+      int i = tid;
+      asm("" : "+v"(i));  // formed here: addresses kept for it through the loop would spill
+      if (i < 16) reinterpret_cast<int32_t*>(s_tasks + turn)[i] = reinterpret_cast<const int32_t*>(p)[i];
       __syncthreads();
       start(false);
     }
@@ -401,7 +413,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       constexpr int NP = decltype(planes)::n;
       bf16x8 q[D / 16][NQ];
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) query_planes(qraw[c], pl.qmul, q[c]);
+      for (int c = 0; c < D / 16; ++c) load_query(a, pl.qmul, q0 + 16 * c, true, q[c]);
 #pragma unroll
       for (int d = 0; d < S; ++d)
 #pragma unroll
@@ -650,10 +662,11 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
           }
       }
     } else if (busy) {
-      const int64_t slot = (int64_t)done_head * pl.head[1] + done.slot + done.part;
+      const int slot = done_head * pl.head[1] + done.slot + done.part;
       if (tid == 0) pl.records[slot] = JoinRecord{done.part == 0 ? done.parts : 0, done.row, done_head, done.tile};
-      const int r0 = wave * 32 + n32;
-      float* dst = pl.part + (slot * ROWS + r0) * D + 4 * h;
+      int r0 = wave0 * 32 + n32;
+      asm("" : "+v"(r0));  // formed here: addresses kept for it through the loop would spill
+      float* dst = pl.part + ((int64_t)slot * ROWS + r0) * D + 4 * h;
 #pragma unroll
       for (int d = 0; d < S; ++d)
 #pragma unroll
@@ -668,7 +681,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
 }
 
 // Joins split items, a wave per row, and clears rows whose query tile no key
-// tile belongs to.
+// tile belongs to.  16 parts of 16 x 256 rows (33 MB): 11 us.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ SplitItem s_list[kPrefillSlots];

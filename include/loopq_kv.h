@@ -121,7 +121,8 @@ int32_t loopq_kv_trim(const loopq_kv_table* in_host, int32_t page_size, int32_t 
 
 /* Close the holes: with L pages in use (refs > 0), the k-th used page at index
  * L or above moves to the k-th free page below L, so that pages L and above
- * are free; table and refs follow.  page_map (int32 [num_pages]) receives each
+ * are free; table and refs follow (an entry whose page has no holder by refs
+ * becomes -1).  page_map (int32 [num_pages]) receives each
  * used page's new index, -1 for a free one, for holders outside the table.
  * info = {L, pages moved}.  out may be in itself. */
 int32_t loopq_kv_compact(const loopq_kv_pool* pool_host, const loopq_kv_table* in_host,

@@ -5,7 +5,7 @@ numpy in 64 bits for the attention."""
 import numpy as np
 
 U = 2.0 ** -24   # unit roundoff of fp32
-UB = 2.0 ** -9   # unit roundoff of bf16 (8 significant bits)
+UB = 2.0 ** -9   # half of bf16's unit roundoff (8 significant bits: 2^-8); see tolerance()
 
 
 # ------------------------------------------------------------------ pages
@@ -138,8 +138,9 @@ def attend(q, p, pool, slab, table_row, scale, window, sinks):
 
 def tolerance(out, bound, absum, dtype):
     """What the kernel may be off for a result of this type.  bf16 queries: the
-    weights may be rounded to bf16 before they meet the values (A UB), and the
-    result is rounded to bf16."""
+    weights may be rounded to bf16 before they meet the values (A UB, on average
+    over them), and the result is rounded to bf16; the two together are no less
+    than the rounding of the result alone, 2 UB |out|, since A >= |out|."""
     if dtype == "f32":
         return bound + U * np.abs(out)
     e = bound + UB * absum
