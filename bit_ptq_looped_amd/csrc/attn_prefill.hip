@@ -2,13 +2,14 @@
 // sliding window and sinks (attention.hip has the method).
 //
 // Bound by arithmetic where prompts are long: 2 prompts of 8192 tokens, 16 heads of
-// 128, bf16: 0.55 TFLOP in 560 us, 980 TFLOP/s (a large bf16 matrix product
+// 128, bf16: 0.55 TFLOP in 556 us, 990 TFLOP/s (a large bf16 matrix product
 // reaches 1263 here); the shader clock reads 1.7 GHz meanwhile, so that what counts is
 // work per key tile, 2.1 us for 256 rows.  Steps on the way: products of 128 rows
 // from K and V through registers 1438 us; copied to LDS without registers 887; the
 // reference moved only when left behind, reads ahead of the products, tasks by XCD
 // 655; 256 rows, a ring of buffers, heads in blocks 608; tiles without masks and
-// checks as runs of numbers 561.  Without effect: three buffers instead of four,
+// checks as runs of numbers 563; one branch a tile for all that is rare, queries
+// loaded after the first tiles, no spills 552.  Without effect: three buffers instead of four,
 // barriers split in two, wave priorities, other mixes of products and vector work.
 #include "attn_core.h"
 
@@ -681,7 +682,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
 }
 
 // Joins split items, a wave per row, and clears rows whose query tile no key
-// tile belongs to.  16 parts of 16 x 256 rows (33 MB): 11 us.
+// tile belongs to.  16 parts of 16 x 256 rows (33 MB): 10.5 us.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a, AttnPlan pl) {
   __shared__ SplitItem s_list[kPrefillSlots];
