@@ -353,15 +353,17 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a, AttnPlan p
 
 template <int D, bool F32>
 hipError_t launch(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
-  // By what the table has room for, since lengths are not known here.  D = 128,
-  // bf16, every row full, us (short, cut): one row of 16 heads: 512 keys 10.8,
-  // 15.2; 1024 keys 16.1, 15.8; 4096 keys 44, 17.  8 rows of 16 heads: 512 keys
-  // 12.2, 17.4; 2048 keys 28, 35; 8192 keys 125, 112.  64 rows of 20 heads: 256
-  // keys 45, 41; 2048 keys 239, 255.
+  // By what the table has room for, since lengths are not known here, and the
+  // number of items: with one item a work-group, more than 640 queue up, and the
+  // cut line's second launch is the smaller cost.  D = 128, bf16, every row
+  // full, us (short, cut): 16 items: 128 keys 6.0, 12.6; 512 keys 10.3, 12.7; 1024
+  // keys 15.2, 12.7; 4096 keys 43, 15.  128 items: 512 keys 11.4, 14.8; 2048 keys 27,
+  // 32; 4096 keys 54, 52.  640 items: 128 keys 19.1, 21.1; 512 keys 37.4, 37.7.  1280
+  // items: 128 keys 31, 28; 512 keys 69, 66; 2048 keys 237, 249.
   const int items = a.heads * ((a.group + kDecodeRows - 1) / kDecodeRows);
-  const int64_t room = (int64_t)a.width << a.page_shift;
-  if (room <= 512 || (room <= 2048 && (int64_t)a.rows * items >= 128)) {
-    decode_short_kernel<D, F32><<<a.rows * items, 64 * kShortWaves, 0, s>>>(a, pl);
+  const int64_t room = (int64_t)a.width << a.page_shift, n = (int64_t)a.rows * items;
+  if (room <= 512 ? n <= 640 : room <= 2048 && n >= 128) {
+    decode_short_kernel<D, F32><<<(unsigned)n, 64 * kShortWaves, 0, s>>>(a, pl);
     return hipGetLastError();
   }
   const int lds = (a.rows + 1) * 8;
