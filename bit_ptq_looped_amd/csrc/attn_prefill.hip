@@ -339,6 +339,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     r.pos = t.len - t.n + r.qi;
     return r;
   };
+  const auto has_rows = [&](const PrefillTask& t) { return (int64_t)t.tile * ROWS + wave0 * 32 < (int64_t)t.n * a.group; };  // this wave
   // the task's first tiles on their way; no copy may be under way
   const auto start = [&](bool fetched) {
     const PrefillTask t = read_task(s_tasks[turn]);
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
     base = reinterpret_cast<const char*>(a.pool + (((int64_t)kvh << a.page_shift) * D) + (W == 8 && wave0 >= 4 ? a.plane : 0)) + my_off;
     const Row r = row_of(t, kvh);
     pos = r.pos;
-    busy = (int64_t)t.tile * ROWS + wave0 * 32 < (int64_t)t.n * a.group;
+    busy = has_rows(t);
     q0 = (int64_t)(t.first + r.qi) * a.ldq + (int64_t)r.hq * D + 8 * h;
     paged = read_pages(0, fetched);
 #pragma unroll
@@ -662,7 +663,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
               *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at + 32 * d + 2 * r) = v;
           }
       }
-    } else if (busy) {
+    } else if (has_rows(done)) {  // `busy` is the next task's by now
       const int slot = done_head * pl.head[1] + done.slot + done.part;
       if (tid == 0) pl.records[slot] = JoinRecord{done.part == 0 ? done.parts : 0, done.row, done_head, done.tile};
       int r0 = wave0 * 32 + n32;
