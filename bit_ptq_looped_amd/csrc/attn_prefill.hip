@@ -625,12 +625,13 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       kvh = __builtin_amdgcn_readfirstlane(s_head);
       start(true);
     }
+    const Row mine = row_of(done, done_head);  // `pos` is the next task's by now
     if (careful) {
       for (int j = key_in(done.k0, done.head, done.from, 0); j <= done.hi; ++j) {
         const int tile = j >> 6, i = tile < done.head ? tile : tile - done.from + done.head;
         if ((tile >= done.head && tile < done.from) || i < done.k0 || i >= done.k1) continue;
         const int page = a.table[(int64_t)done.row * a.width + (j >> a.page_shift)];
-        if ((uint32_t)page >= (uint32_t)a.num_pages || !sees(a, pos, j)) continue;
+        if ((uint32_t)page >= (uint32_t)a.num_pages || !sees(a, mine.pos, j)) continue;
         const uint16_t* v = a.pool + a.plane + page * a.page_stride + (((int64_t)done_head << a.page_shift) + (j & in_page)) * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < S; ++d)
@@ -647,7 +648,6 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
       }
     }
     l += __shfl_xor(l, 32, 64);
-    const Row mine = row_of(done, done_head);
     if (done.parts == 1) {
       const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
       if (mine.has) {

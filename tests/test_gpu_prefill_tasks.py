@@ -2,7 +2,10 @@
 results after the next one's first tiles are on their way, and the two differ in
 rows, positions and parts."""
 
+import math
+
 import pytest
+import torch
 
 from test_gpu_attention import Case
 
@@ -30,3 +33,22 @@ def test_parts_followed_by_a_task_with_fewer_rows(lq, dtype, lens, news, heads, 
     some = one_of_every_32_rows(c, heads, group)
     c.queries = lambda: some
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,news,heads,group,window,sinks", [
+    ([3000], [3000], 24, 1, 0, 0), ([3000], [3000], 24, 1, 700, 2), ([2500, 1111, 1800], [1500, 1111, 900], 12, 2, 0, 0)])
+def test_a_value_that_some_queries_see_among_many_tasks(lq, lens, news, heads, group, window, sinks, dtype):
+    """NaN or infinity in a token's values reaches the queries that see it, and no other, whatever task comes next."""
+    c = Case(lens, heads, group, 64, 16, window, sinks, dtype=dtype, slabs=1, slab=0, news=news, trash=False)
+    want = c.run()
+    assert torch.isfinite(want).all()
+    odd = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+    for b, j, col, value in ((0, 700, 63, math.inf), (len(lens) - 1, 1000, 5, math.nan)):
+        c.pool[c.table[b][j // 16], 0, 1, :, j % 16, col] = value
+        for t, row, p in c.queries():
+            odd[t, :, col] |= row == b and p >= j and (not window or p - j < window)
+    got = c.run()
+    assert torch.equal(~torch.isfinite(got), odd)
+    rest = ~odd.any(-1).any(-1)
+    assert rest.any() and torch.equal(got[rest], want[rest])
