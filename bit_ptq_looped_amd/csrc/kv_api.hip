@@ -207,7 +207,8 @@ int32_t loopq_kv_write(const loopq_kv_pool* pool, int32_t slab, const loopq_kv_t
   st = check_rows(k, ldk, width, tokens, dtype);
   if (st == LOOPQ_OK) st = check_rows(v, ldv, width, tokens, dtype);
   if (st != LOOPQ_OK) return st;
-  if (tokens * (width / 8) >= ((int64_t)1 << 39)) return LOOPQ_ERR_UNSUPPORTED;  // work-groups of one launch
+  // a launch has fewer than 2^32 work-items: eight elements each, in work-groups of 256
+  if (tokens * (width / 8) > ((int64_t)1 << 32) - 256) return LOOPQ_ERR_UNSUPPORTED;
   KvWriteArgs a;
   a.plane = (int64_t)pool->heads * pool->page_size * pool->head_dim;
   a.page_stride = pool->slabs * 2 * a.plane;

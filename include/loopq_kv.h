@@ -92,7 +92,8 @@ int32_t loopq_kv_reserve(const loopq_kv_table* in_host, int32_t page_size, const
  * k, v [tokens][heads][head_dim] in `dtype`, tokens ldk and ldv elements apart
  * (slices of a fused q|k|v row qualify), 16-byte aligned rows; fp32 is rounded
  * to bf16, to nearest, ties to even.  A token whose position has no page is
- * dropped; tokens past cu[rows] are not read. */
+ * dropped; tokens past cu[rows] are not read.  tokens * heads * head_dim is at most
+ * 2^35 - 2048 (LOOPQ_ERR_UNSUPPORTED). */
 int32_t loopq_kv_write(const loopq_kv_pool* pool_host, int32_t slab, const loopq_kv_table* table_host,
                        const int32_t* cu, const void* k, int64_t ldk, const void* v, int64_t ldv,
                        int32_t dtype, int32_t tokens, void* stream);

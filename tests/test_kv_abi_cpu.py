@@ -164,3 +164,12 @@ def test_attention_arguments(lib, prefill):
     assert call(hq=1 << 15) == UNSUPPORTED
     t.rows = 0
     assert call(q=None, out=None) == 0
+
+
+def test_a_write_larger_than_a_launch_is_refused(lib):
+    """A launch has fewer than 2^32 work-items, eight elements each, 256 of them a work-group."""
+    call = lambda heads, dim, n: lib.loopq_kv_write(R(pool(heads=heads, head_dim=dim)), 0, R(table()), FAKE, FAKE, heads * dim, FAKE,
+                                                    heads * dim, 1, n, None)  # noqa: E731
+    assert call(2048, 128, 1 << 17) == UNSUPPORTED  # 2^32
+    assert call(2, 64, (1 << 28) - 15) == UNSUPPORTED  # 2^32 - 240: its last work-group ends at 2^32
+    assert call(2, 64, (1 << 31) - 1) == UNSUPPORTED
