@@ -362,7 +362,8 @@ hipError_t launch(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
   // items: 128 keys 31, 28; 512 keys 69, 66; 2048 keys 237, 249.
   const int items = a.heads * ((a.group + kDecodeRows - 1) / kDecodeRows);
   const int64_t room = (int64_t)a.width << a.page_shift, n = (int64_t)a.rows * items;
-  if (room <= 512 ? n <= 640 : room <= 2048 && n >= 128) {
+  const bool launchable = n * (64 * kShortWaves) < ((int64_t)1 << 32);  // work-items of one launch
+  if (launchable && (room <= 512 ? n <= 640 : room <= 2048 && n >= 128)) {
     decode_short_kernel<D, F32><<<(unsigned)n, 64 * kShortWaves, 0, s>>>(a, pl);
     return hipGetLastError();
   }

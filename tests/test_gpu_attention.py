@@ -392,3 +392,19 @@ def test_pages_past_four_gigabytes(lq):
     assert torch.equal(pool[t.table[0, 1].item(), 15, 0, :, 399 - 256], k[0].to(torch.bfloat16))
     kv.loopq_kv_copy_pages(pool, i32([pages - 1]), pool, i32([pages - 3]))
     assert torch.equal(pool[pages - 3, 15], pool[pages - 1, 15])
+
+
+def test_decode_of_more_items_than_one_launch_has_work_groups_for(lq):
+    """8192 rows of 1024 heads, in a table with room for 1024 tokens: a work-group an item would be 2^32 work-items."""
+    lens = [i % 37 for i in range(32)]
+    c = Case(lens, 1024, 1, 64, 8, slabs=1, slab=0, width=126)
+    assert 512 < 8 * c.width <= 2048
+    t = kv.KVTable(c.t.table.repeat(256, 1), c.t.lens.repeat(256), c.t.refs)
+    q = c.q.repeat(256, 1, 1)
+    out = torch.full_like(q, 7.0)
+    kv.loopq_attn_decode(c.pool, 0, t, q, out, kv.empty_attn_workspace(c.pool, 8192, 1024, 8192), c.scale)
+    pool, q32 = c.pool.double().cpu().numpy(), c.q.double().cpu().numpy()
+    each = [ref.attend(q32[b], n - 1, pool, 0, c.table[b], c.scale, 0, 0) for b, n in enumerate(lens)]
+    want = torch.tensor(np.stack([w for w, _, _ in each]), device="cuda")
+    tol = torch.tensor(np.stack([ref.tolerance(*x, "bf16") for x in each]), device="cuda")
+    assert all(((some.double() - want).abs() <= tol).all() for some in out.split(32))
