@@ -540,9 +540,10 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
           for (int t = 0; t < 2; ++t) tops[t] = fmaxf(tops[t], s[t][r]);
         const float top = max_halves(fmaxf(tops[0], tops[1])) * pl.c;
         // the reference follows only when it is left far behind: weights up to 2^8
-        // are as exact, and rescaling costs a pass over o
+        // are as exact, and rescaling costs a pass over o; each query's by its own
+        // scores, so that keys which only its neighbours see leave no trace
         if (__any(top > m + 8.0f)) {
-          const float mn = fmaxf(m, top);
+          const float mn = top > m + 8.0f ? top : m;
           const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
           m = mn;
           l *= f;

@@ -408,3 +408,19 @@ def test_decode_of_more_items_than_one_launch_has_work_groups_for(lq):
     want = torch.tensor(np.stack([w for w, _, _ in each]), device="cuda")
     tol = torch.tensor(np.stack([ref.tolerance(*x, "bf16") for x in each]), device="cuda")
     assert all(((some.double() - want).abs() <= tol).all() for some in out.split(32))
+
+
+@BOTH
+@pytest.mark.parametrize("window,group", [(0, 1), (0, 3), (90, 1)])
+def test_keys_that_a_query_does_not_see_leave_no_trace(lq, window, group, dtype):
+    """Not even in the last bit, where queries beside it see them and their scores are large."""
+    c = Case([200, 130], 2, group, 64, 16, window, 3, dtype=dtype, news=[200, 100], trash=False)
+    want = c.run()
+    j = 100
+    for b in range(2):
+        c.pool[c.table[b][j // 16], c.slab, 0, :, j % 16] *= 40
+        c.pool[c.table[b][j // 16], c.slab, 1, :, j % 16] *= -3
+    got = c.run()
+    sees = torch.tensor([p >= j and (not window or p - j < window) for _, _, p in c.queries()], device="cuda")
+    assert torch.equal(got[~sees], want[~sees])
+    assert not torch.equal(got[sees], want[sees])
