@@ -150,9 +150,19 @@ int32_t loopq_attn_workspace_bytes(int32_t queries, int32_t heads_q, int32_t row
  * the cache); key j is visible to a query at position p if 0 <= j <= p, the
  * table has a page for j, and window == 0 or p - j < window or j < sinks.
  * out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) over the visible keys,
- * s_j = scale * (q . k_j), m their maximum; 0 where no key is visible.  Sums are
- * held in fp32.  Keys and values at hidden positions are not used, whatever
- * they hold.  scale is finite; window, sinks >= 0. */
+ * s_j = scale * (q . k_j), m their maximum; 0 where no key is visible.  Keys and
+ * values at hidden positions are not used, whatever they hold.  scale is finite;
+ * window, sinks >= 0.
+ *
+ * Precision: sums are held in fp32.  fp32 queries and the weights they give
+ * enter the products with 24 bits, weights of bf16 queries with 16 (see prefill).
+ * Range: the magnitudes of the values that a query sees add up to less than 2^119
+ * in every column; past that, results may be infinite (weights are taken against
+ * a reference that their maximum may exceed by 2^8).
+ * Infinities and NaN: a value that is infinite or NaN makes its column infinite or
+ * NaN (either of them) for every query that sees it, however small its weight,
+ * and reaches no other query.  A score of -infinity is a weight of 0, and out is 0
+ * if all are; a score of +infinity or NaN makes the whole head's result NaN. */
 int32_t loopq_attn_decode(const loopq_kv_pool* pool_host, int32_t slab, const loopq_kv_table* table_host,
                           const void* q, int64_t ldq, int32_t dtype, int32_t heads_q, float scale,
                           int32_t window, int32_t sinks, void* out, int64_t ldo, void* workspace,
@@ -162,7 +172,10 @@ int32_t loopq_attn_decode(const loopq_kv_pool* pool_host, int32_t slab, const lo
  * cu[b+1] - 1 of q (device int32 [rows + 1], ascending from 0), the last of the
  * row's lens[b] tokens, query i of n at position lens[b] - n + i (nothing is
  * visible at a negative position).  q, out [queries][heads_q][head_dim]; rows of
- * out past cu[rows] are not written. */
+ * out past cu[rows] are not written.  Weights of bf16 queries are rounded to one
+ * bf16 (8 bits) before they meet the values, and the sum is that of the rounded
+ * weights; they keep 16 bits where window < 256 (and not 0) or the queries lie
+ * among the first 255 tokens.  fp32 queries keep 24 bits throughout. */
 int32_t loopq_attn_prefill(const loopq_kv_pool* pool_host, int32_t slab, const loopq_kv_table* table_host,
                            const int32_t* cu, const void* q, int64_t ldq, int32_t dtype, int32_t queries,
                            int32_t heads_q, float scale, int32_t window, int32_t sinks, void* out,

@@ -424,3 +424,56 @@ def test_keys_that_a_query_does_not_see_leave_no_trace(lq, window, group, dtype)
     sees = torch.tensor([p >= j and (not window or p - j < window) for _, _, p in c.queries()], device="cuda")
     assert torch.equal(got[~sees], want[~sees])
     assert not torch.equal(got[sees], want[sees])
+
+
+@BOTH
+@pytest.mark.parametrize("lens,news,width", [([300], None, 19), ([300], None, 140), ([5000], None, 320), ([300], [300], 20), ([5000], [40], 320)])
+def test_values_that_are_not_finite_stay_so_whatever_their_weight(lq, lens, news, width, dtype):
+    """Scores fall from one end of the row to the other so that weights are 0 in 32 bits at the far end."""
+    c = Case(lens, 2, 1, 64, 16, dtype=dtype, news=news, width=width)
+    n = lens[0]
+    for j in range(n):  # scores from 0 down to -10 n, the largest at the row's last token
+        c.pool[c.table[0][j // 16], c.slab, 0, :, j % 16] = 0
+        c.pool[c.table[0][j // 16], c.slab, 0, :, j % 16, 0] = -80.0 * (n - 1 - j)
+    c.q[:, :, 0] = 1
+    want = c.run()
+    assert torch.isfinite(want).all()
+    odd = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+    for j, col, value in ((0, 3, math.nan), (1, 40, math.inf), (n // 2, 41, -math.inf), (n - 1, 63, math.inf)):
+        c.pool[c.table[0][j // 16], c.slab, 1, :, j % 16, col] = value
+        for t, _, p in c.queries():
+            odd[t, :, col] |= p >= j
+    got = c.run()
+    assert torch.equal(~torch.isfinite(got), odd)
+    assert torch.equal(got[~odd], want[~odd])
+
+
+@BOTH
+@pytest.mark.parametrize("news,width", [(None, 13), (None, 140), ([200], 13)])
+def test_scores_that_are_not_finite(lq, news, width, dtype):
+    """All scores -infinity: 0; one of +infinity or NaN: NaN in every column of that head."""
+    c = Case([200], 3, 1, 64, 16, dtype=dtype, news=news, width=width, seed=5)
+    c.q[:, :, 9] = 1
+    want = c.run()
+    for j in range(200):
+        c.pool[c.table[0][j // 16], c.slab, 0, 0, j % 16, 9] = -math.inf
+    c.pool[c.table[0][100 // 16], c.slab, 0, 1, 100 % 16, 9] = math.inf
+    got = c.run()
+    sees = torch.tensor([p >= 100 for _, _, p in c.queries()], device="cuda")
+    assert not got[:, 0].any()
+    assert got[sees, 1].isnan().all() and torch.equal(got[~sees, 1], want[~sees, 1])
+    assert torch.equal(got[:, 2], want[:, 2])
+    c.pool[c.table[0][100 // 16], c.slab, 0, 1, 100 % 16, 9] = math.nan
+    got = c.run()
+    assert got[sees, 1].isnan().all() and torch.equal(got[~sees, 1], want[~sees, 1])
+
+
+@BOTH
+@pytest.mark.parametrize("lens,news,width", [([400], None, 26), ([400], None, 140), ([400], [400], 26), ([2000, 300], [90, 300], 130)])
+def test_large_values(lq, lens, news, width, dtype):
+    """Values whose magnitudes add up to less than 2^119: a power of two, which scales every sum exactly."""
+    c = Case(lens, 2, 2, 64, 16, dtype=dtype, news=news, width=width, qmul=4.0)
+    want = c.run()
+    c.pool[:, :, 1] *= 2.0 ** 105  # at most 2000 values of up to 2^2.5
+    got = c.run()
+    assert torch.isfinite(got).all() and torch.equal(got, want * 2.0 ** 105)
