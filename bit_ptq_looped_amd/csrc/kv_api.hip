@@ -102,6 +102,16 @@ int32_t check_rows(const void* p, int64_t ld, int64_t width, int64_t rows, int d
   return LOOPQ_OK;
 }
 
+// whether two matrices of `rows` rows of `width` bytes share a byte; columns of the
+// same wider rows do not
+bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t width, int64_t rows) {
+  if (!overlap(a, (rows - 1) * lda + width, b, (rows - 1) * ldb + width)) return false;
+  if (rows == 1 || lda != ldb) return true;
+  const int64_t far = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) % lda;
+  const int64_t at = far < 0 ? far + lda : far;  // where a row of b starts, from that of a before it
+  return at < width || at > lda - width;
+}
+
 int32_t run_attn(const loopq_kv_pool* pool, int32_t slab, const loopq_kv_table* table, const int32_t* cu, const void* q,
                  int64_t ldq, int32_t dtype, int32_t queries, int32_t heads_q, float scale, int32_t window,
                  int32_t sinks, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
@@ -119,9 +129,8 @@ int32_t run_attn(const loopq_kv_pool* pool, int32_t slab, const loopq_kv_table* 
   st = check_rows(q, ldq, width, queries, dtype);
   if (st == LOOPQ_OK) st = check_rows(out, ldo, width, queries, dtype);
   if (st != LOOPQ_OK) return st;
-  const size_t item = dtype == LOOPQ_F32 ? 4 : 2;
-  if (overlap(q, ((queries - 1) * ldq + width) * item, out, ((queries - 1) * ldo + width) * item))
-    return LOOPQ_ERR_INVALID_ARG;
+  const int item = dtype == LOOPQ_F32 ? 4 : 2;
+  if (rows_overlap(q, ldq * item, out, ldo * item, width * item, queries)) return LOOPQ_ERR_INVALID_ARG;
   st = check_workspace(workspace, workspace_bytes, attn_workspace_bytes(queries, heads_q, table->rows, pool->head_dim));
   if (st != LOOPQ_OK) return st;
   AttnArgs a;

@@ -145,10 +145,11 @@ int32_t loopq_attn_workspace_bytes(int32_t queries, int32_t heads_q, int32_t row
 
 /* Attention of one new token per row over the row's cached tokens in one slab.
  * q, out [rows][heads_q][head_dim] in `dtype` (fp32 or bf16), rows ldq and ldo
- * elements apart, 16-byte aligned rows; query head h reads key head
- * h / (heads_q / heads).  The query of row b is its token lens[b] - 1 (already in
- * the cache); key j is visible to a query at position p if 0 <= j <= p, the
- * table has a page for j, and window == 0 or p - j < window or j < sinks.
+ * elements apart, 16-byte aligned rows (with ldq = ldo also columns of the same
+ * wider rows); query head h reads key head h / (heads_q / heads).  The query of
+ * row b is its token lens[b] - 1 (already in the cache); key j is visible to a
+ * query at position p if 0 <= j <= p, the table has a page for j, and window == 0
+ * or p - j < window or j < sinks.
  * out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) over the visible keys,
  * s_j = scale * (q . k_j), m their maximum; 0 where no key is visible.  Keys and
  * values at hidden positions are not used, whatever they hold.  scale is finite;

@@ -477,3 +477,15 @@ def test_large_values(lq, lens, news, width, dtype):
     c.pool[:, :, 1] *= 2.0 ** 105  # at most 2000 values of up to 2^2.5
     got = c.run()
     assert torch.isfinite(got).all() and torch.equal(got, want * 2.0 ** 105)
+
+
+@BOTH
+@pytest.mark.parametrize("news", [None, [130, 9]])
+def test_out_beside_the_queries_in_one_buffer(lq, news, dtype):
+    c = Case([130, 40], 2, 2, 64, 16, dtype=dtype, news=news)
+    n = c.hq * 64
+    wide = torch.full((c.q_tokens, 2 * n + 8), 5.0, dtype=c.q.dtype, device="cuda")
+    wide[:, :n] = c.q.flatten(1)
+    got = c.run(wide[:, :n].unflatten(1, (c.hq, 64)), wide[:, n + 8:].unflatten(1, (c.hq, 64)))
+    assert torch.equal(got, c.run())
+    assert torch.equal(wide[:, :n], c.q.flatten(1)) and (wide[:, n:n + 8] == 5).all()

@@ -173,3 +173,24 @@ def test_a_write_larger_than_a_launch_is_refused(lib):
     assert call(2048, 128, 1 << 17) == UNSUPPORTED  # 2^32
     assert call(2, 64, (1 << 28) - 15) == UNSUPPORTED  # 2^32 - 240: its last work-group ends at 2^32
     assert call(2, 64, (1 << 31) - 1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_columns_of_the_same_rows_do_not_overlap(lib, prefill, dt):
+    """q and out in one wider row of 600 elements; a call that gets past the check lacks a workspace."""
+    p, t, item = pool(), table(), 2 if dt else 4
+
+    def call(q, out, ldq=600, ldo=600, n=4):
+        tail = (4, 1.0, 0, 0, FAKE + OTHER + out * item, ldo, None, 0, None)
+        if prefill:
+            return lib.loopq_attn_prefill(R(p), 0, R(t), FAKE, FAKE + OTHER + q * item, ldq, dt, n, *tail)
+        return lib.loopq_attn_decode(R(p), 0, R(t), FAKE + OTHER + q * item, ldq, dt, *tail)
+
+    for q, out in ((0, 256), (256, 0), (8, 344), (344, 8), (0, 4 * 600), (0, 256 + 600), (256 + 1200, 0)):
+        assert call(q, out) == WORKSPACE
+    for q, out in ((0, 0), (0, 248), (248, 0), (0, 352), (352, 0), (0, 600), (0, 592), (1200, 8), (8, 1200)):
+        assert call(q, out) == INVALID
+    assert call(0, 256, ldo=608) == INVALID  # rows that drift apart
+    if prefill:
+        assert call(0, 256, n=1) == WORKSPACE and call(0, 248, n=1) == INVALID
