@@ -299,7 +299,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void decode_short_kernel(AttnA
   __syncthreads();
   const int heads = min(kDecodeRows, a.group - gt * kDecodeRows);
   for (int e = tid; e < heads * D; e += 64 * kShortWaves) {
-    const int r = e / D, d = e - r * D;
+    const int r = e / D;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kShortWaves; ++w) top = fmaxf(top, s_m[w][r]);
