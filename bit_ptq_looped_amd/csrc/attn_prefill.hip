@@ -2,8 +2,8 @@
 // sliding window and sinks (attention.hip has the method).
 //
 // Bound by arithmetic where prompts are long: 2 prompts of 8192 tokens, 16 heads of
-// 128, bf16: 0.55 TFLOP in 556 us, 990 TFLOP/s (a large bf16 matrix product
-// reaches 1263 here); the shader clock reads 1.7 GHz meanwhile, so that what counts is
+// 128, bf16: 0.55 TFLOP in 551 to 567 us, 970 to 998 TFLOP/s (a large bf16 matrix product
+// reaches 1263 to 1302 here); the shader clock reads 1.7 GHz meanwhile, so that what counts is
 // work per key tile, 2.1 us for 256 rows.  Steps on the way: products of 128 rows
 // from K and V through registers 1438 us; copied to LDS without registers 887; the
 // reference moved only when left behind, reads ahead of the products, tasks by XCD
@@ -11,6 +11,8 @@
 // checks as runs of numbers 563; one branch a tile for all that is rare, queries
 // loaded after the first tiles, no spills 552.  Without effect: three buffers instead of four,
 // barriers split in two, wave priorities, other mixes of products and vector work.
+// fp32 queries, the same prompts: 1555 us, 354 TFLOP/s where three planes for one leave
+// a third of 1300, since one wave a SIMD takes turns between products and vector work.
 #include "attn_core.h"
 
 namespace loopq {
@@ -203,7 +205,8 @@ __device__ __forceinline__ void sync_lds() {
 // that no work-group keeps one waiting while another is idle, its description and
 // page entries are fetched during the last three tiles, and its first tiles are on
 // their way while results are stored (12 rows with 1500 new tokens, 32 query heads of
-// 96, window 1000: asked for at the start 209 us, late 190, fetched ahead 180).  Keys that no query of the item
+// 96, window 1000: asked for at the start 209 us, late 190, fetched ahead 180; 171
+// with the steps above).  Keys that no query of the item
 // sees are read from a line of zeros.  fp32 queries hold three planes in registers
 // and take half the rows.
 template <int D, bool F32, int W>
@@ -255,6 +258,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void prefill_attn_kernel(AttnArgs a,
   }
 
   int turn = 0, kvh = 0;  // the task at work is s_tasks[turn]: scalar registers are short
+  // What follows down to q0 is set by start(), and is the next task's from there on:
+  // results are stored by the finished task's own description.
   // Its tiles by number n.  A tile is copied plainly if every key of it is seen by
   // some query, and taken whole if every key is seen by every query; both are
   // runs of numbers (tiles of sinks count as neither), as long as the pages are

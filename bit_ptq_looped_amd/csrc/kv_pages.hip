@@ -217,6 +217,8 @@ __device__ __forceinline__ void copy_chunk(const char* src, char* dst, int64_t a
     if (tid + 256 * i < n) d[tid + 256 * i] = v[i];
 }
 
+// Bound by the bytes: 2000 pages of 1 MB 829 us, 5.1 TB/s read and written; 64 pages
+// of 0.5 MB 12.7 us.
 __global__ __launch_bounds__(256) void copy_pages_kernel(const char* src_pool, int src_pages, const int32_t* src,
                                                          char* dst_pool, int dst_pages, const int32_t* dst, int count,
                                                          int64_t page_bytes) {
