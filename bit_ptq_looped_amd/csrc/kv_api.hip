@@ -2,22 +2,11 @@
 // include/loopq_kv.h): host-side checks and dispatch on the caller's stream.
 #include <math.h>
 
-#include "kv_internal.h"
+#include "arg_checks.h"
 
 using namespace loopq;
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
-
-int32_t hip_status(hipError_t e) { return e == hipSuccess ? LOOPQ_OK : LOOPQ_ERR_HIP; }
-
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + bn && y < x + an;
-}
 
 int32_t check_page_size(int n) {
   if (n <= 0) return LOOPQ_ERR_INVALID_ARG;
@@ -45,6 +34,10 @@ int64_t page_bytes(const loopq_kv_pool* p) {
   return (int64_t)p->slabs * 2 * p->heads * p->page_size * p->head_dim * 2;
 }
 
+}  // namespace
+
+namespace loopq {
+
 int32_t check_pool(const loopq_kv_pool* p) {
   if (!p) return LOOPQ_ERR_INVALID_ARG;
   int32_t st = check_shape(p->num_pages, p->slabs, p->heads, p->page_size, p->head_dim);
@@ -70,6 +63,10 @@ KvTable table_of(const loopq_kv_table* t) {
   return KvTable{t->table, t->lens, t->refs, t->rows, t->max_pages, t->num_pages};
 }
 
+}  // namespace loopq
+
+namespace {
+
 // in and out of one call: the same three buffers, or nothing shared
 int32_t check_pair(const loopq_kv_table* a, const loopq_kv_table* b, bool may_be_same) {
   int32_t st = check_table(a);
@@ -86,30 +83,6 @@ int32_t check_pair(const loopq_kv_table* a, const loopq_kv_table* b, bool may_be
     for (int j = 0; j < 3; ++j)
       if (na[i] && nb[j] && overlap(pa[i], na[i], pb[j], nb[j])) return LOOPQ_ERR_INVALID_ARG;
   return LOOPQ_OK;
-}
-
-int32_t check_workspace(const void* ws, size_t have, size_t need) {
-  if (!ws || have < need) return LOOPQ_ERR_WORKSPACE;
-  return aligned(ws, 256) ? LOOPQ_OK : LOOPQ_ERR_ALIGNMENT;
-}
-
-// rows of `width` elements `ld` apart, 16-byte aligned each
-int32_t check_rows(const void* p, int64_t ld, int64_t width, int64_t rows, int dtype) {
-  if (!p) return LOOPQ_ERR_INVALID_ARG;
-  if (rows > 1 && ld < width) return LOOPQ_ERR_INVALID_ARG;
-  const int item = dtype == LOOPQ_F32 ? 4 : 2;
-  if (!aligned(p, 16) || (rows > 1 && (ld * item) % 16)) return LOOPQ_ERR_ALIGNMENT;
-  return LOOPQ_OK;
-}
-
-// whether two matrices of `rows` rows of `width` bytes share a byte; columns of the
-// same wider rows do not
-bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t width, int64_t rows) {
-  if (!overlap(a, (rows - 1) * lda + width, b, (rows - 1) * ldb + width)) return false;
-  if (rows == 1 || lda != ldb) return true;
-  const int64_t far = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) % lda;
-  const int64_t at = far < 0 ? far + lda : far;  // where a row of b starts, from that of a before it
-  return at < width || at > lda - width;
 }
 
 int32_t run_attn(const loopq_kv_pool* pool, int32_t slab, const loopq_kv_table* table, const int32_t* cu, const void* q,
@@ -129,8 +102,8 @@ int32_t run_attn(const loopq_kv_pool* pool, int32_t slab, const loopq_kv_table* 
   st = check_rows(q, ldq, width, queries, dtype);
   if (st == LOOPQ_OK) st = check_rows(out, ldo, width, queries, dtype);
   if (st != LOOPQ_OK) return st;
-  const int item = dtype == LOOPQ_F32 ? 4 : 2;
-  if (rows_overlap(q, ldq * item, out, ldo * item, width * item, queries)) return LOOPQ_ERR_INVALID_ARG;
+  const int item = item_bytes(dtype);
+  if (rows_overlap(q, ldq * item, width * item, out, ldo * item, width * item, queries)) return LOOPQ_ERR_INVALID_ARG;
   st = check_workspace(workspace, workspace_bytes, attn_workspace_bytes(queries, heads_q, table->rows, pool->head_dim));
   if (st != LOOPQ_OK) return st;
   AttnArgs a;
