@@ -9,15 +9,38 @@ non-zero status raises :class:`~bit_ptq_looped_amd.loopq.LoopQError`.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 from . import kv, loopq
+from .kv import KVTable, _ints, _pool, _ref, _rows3, _table
 from .loopq import _check, _dtype_code, _ptr, _stream
+
+LOOPQ_ROPE_HALF, LOOPQ_ROPE_PAIRS = 0, 1
+LOOPQ_ROPE_PLAIN, LOOPQ_ROPE_LINEAR, LOOPQ_ROPE_BASE, LOOPQ_ROPE_PARTS = 0, 1, 2, 3
+
+
+class Rope(NamedTuple):
+    """Frequencies float64 [rot_dim / 2] on the device (radians a position),
+    which elements form a pair, and the factor of the turned ones."""
+    inv_freq: "torch.Tensor"  # noqa: F821
+    layout: int = LOOPQ_ROPE_HALF
+    magnitude: float = 1.0
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
 
 _P, _I, _F, _Z, _L, _D = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64,
                           ctypes.c_double)
+_RP = ctypes.POINTER(_Rope)
 # every entry point of include/loopq_block.h with its ctypes signature
 SIGNATURES = {
     "loopq_rms_norm": ([_P, _L, _I, _P, _L, _I, _I, _I, _P, _F, _P, _L, _P, _L, _I, _P, _P, _F, _I, _I, _P], _I),
+    "loopq_rope_frequencies": ([_I, _I, _D, _D, _D, _D, _D, ctypes.POINTER(_D)], _I),
+    "loopq_rope": ([_P, _L, _I, _I, _I, _I, _P, _RP, _P, _L, _P], _I),
+    "loopq_kv_write_rope": ([kv._PP, _I, kv._TP, _P, _RP, _P, _L, _P, _L, _I, _I, _P, _L, _I, _P, _L, _I, _P], _I),
 }
 
 _lib = None
@@ -56,6 +79,22 @@ def _dense(t, what: str, dtype, n: int):
     return _ptr(t)
 
 
+def _rope(r: Rope) -> _Rope:
+    f = r.inv_freq
+    return _Rope(_dense(f, "inv_freq", loopq._torch_mod().float64, 1), 2 * f.numel(), r.layout, r.magnitude)
+
+
+# ----------------------------------------------------------------- host-only calls
+
+def loopq_rope_frequencies(scaling: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0,
+                           length: float = 0.0, low: float = 0.0, high: float = 0.0):
+    """The frequencies of a scaling as a list of rot_dim / 2 floats."""
+    f = (ctypes.c_double * max(rot_dim // 2, 1))()
+    _check(load().loopq_rope_frequencies(scaling, rot_dim, base, factor, length, low, high, f),
+           "loopq_rope_frequencies")
+    return list(f)
+
+
 # ----------------------------------------------------------------- device calls
 
 def loopq_rms_norm(x, weight, eps: float, y=None, residual=None, sum_out=None, codes=None, steps=None,
@@ -78,3 +117,35 @@ def loopq_rms_norm(x, weight, eps: float, y=None, residual=None, sum_out=None, c
         gp = _dense(steps, "steps", torch.float32, rows * (K // 32))
     _check(load().loopq_rms_norm(*xp, *rp, rows, K, wp, eps, sp[0], sp[1], *yp, cp, gp, clip, bits_a, int(per_token),
                                  _on(x, stream)), "loopq_rms_norm")
+
+
+def loopq_rope(x, positions, rope: Rope, out, stream=None):
+    """x, out [tokens][heads][head_dim], positions int32 [tokens]; out may be x itself."""
+    tokens, heads, dim = x.shape
+    xp, ldx = _rows3(x, None, dim, "x")
+    op, ldo = _rows3(out, heads, dim, "out")
+    if out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError("out must have x's type and shape")
+    _check(load().loopq_rope(xp, ldx, _dtype_code(x), tokens, heads, dim, _ints(positions, "positions", tokens),
+                             _ref(_rope(rope)), op, ldo, _on(x, stream)), "loopq_rope")
+
+
+def loopq_kv_write_rope(pool, slab: int, table: KVTable, cu, rope: Rope, k, v, q=None, q_out=None, stream=None):
+    """k turned and v into a slab as the last tokens of each row, q turned into q_out
+    (bfloat16 or float32; q itself if it has that type)."""
+    p = _pool(pool)
+    kp, ldk = _rows3(k, p.heads, p.head_dim, "k")
+    vp, ldv = _rows3(v, p.heads, p.head_dim, "v")
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must have one type and shape")
+    qp = op = None
+    ldq = ldo = heads_q = q_dtype = 0
+    if q is not None:
+        if q.dtype != k.dtype or q.shape[0] != k.shape[0] or q_out is None or q_out.shape != q.shape:
+            raise ValueError("q must have k's type and tokens, q_out its shape")
+        qp, ldq = _rows3(q, None, p.head_dim, "q")
+        op, ldo = _rows3(q_out, None, p.head_dim, "q_out")
+        heads_q, q_dtype = q.shape[1], _dtype_code(q_out)
+    _check(load().loopq_kv_write_rope(_ref(p), slab, _ref(_table(table)), _ints(cu, "cu", table.lens.numel() + 1),
+                                      _ref(_rope(rope)), kp, ldk, vp, ldv, _dtype_code(k), k.shape[0], qp, ldq,
+                                      heads_q, op, ldo, q_dtype, _on(k, stream)), "loopq_kv_write_rope")

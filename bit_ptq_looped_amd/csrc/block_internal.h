@@ -26,4 +26,32 @@ struct NormArgs {
 };
 hipError_t launch_rms_norm(NormArgs a, hipStream_t s);
 
+// One tensor of a rotary call: [tokens][heads][dim], heads side by side.
+struct RopePart {
+  const void* in;
+  void* out;          // null for the keys and values of a cache write
+  int64_t ld_in, ld_out;  // elements
+  int heads;
+  int out_bf16;
+};
+
+// Rotary positions of up to three tensors: q (turned, to out), k (turned) and v
+// (as it is) to the slab.  Without a cache, part[0] alone at given positions.
+struct RopeArgs {
+  RopePart part[3];
+  int in_bf16;
+  int tokens, head_dim, rot, pairs;
+  const double* inv_freq;
+  float magnitude;
+  const int32_t* positions;  // given positions, or null: from the table
+  const int32_t* cu;
+  KvTable t;
+  uint16_t* pool;            // at the slab's keys of page 0
+  int64_t page_stride, plane;
+  int page_shift;
+  int heads;                 // of all parts
+  int split, per;            // waves a token, heads each of them takes
+};
+hipError_t launch_rope(RopeArgs a, hipStream_t s);
+
 }  // namespace loopq

@@ -2,7 +2,7 @@
  * loopq_block.h -- what a block of a looped transformer needs between its
  * quantized linears (include/loopq.h) and the attention (include/loopq_kv.h),
  * for AMD Instinct MI355X (gfx950): the residual's addition with the
- * root-mean-square norm.
+ * root-mean-square norm, and rotary positions.
  *
  * The conventions of loopq.h hold: device pointers unless the name ends in
  * _host, work is enqueued on `stream` and the call returns, the caller owns
@@ -10,7 +10,8 @@
  * of no rows is a no-op.  Buffers must not overlap unless a call says so.
  * "16-byte aligned rows" means the pointer and, where there is more than one
  * row, the distance from a row to the next; columns of the same wider rows
- * qualify.
+ * qualify.  Values read from device memory (positions, lengths, page tables)
+ * are never trusted with an address.
  */
 #ifndef LOOPQ_BLOCK_H
 #define LOOPQ_BLOCK_H
@@ -53,6 +54,65 @@ int32_t loopq_rms_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* 
                        void* sum_out, int64_t lds, void* y, int64_t ldy, int32_t y_dtype,
                        int8_t* codes, float* steps, float clip, int32_t bits_a, int32_t per_token,
                        void* stream);
+
+/* Which elements of a head form the pair that frequency i turns. */
+typedef enum {
+  LOOPQ_ROPE_HALF = 0,  /* x[i] and x[i + rot_dim / 2] */
+  LOOPQ_ROPE_PAIRS = 1  /* x[2 i] and x[2 i + 1] */
+} loopq_rope_layout;
+
+/* Rotary positions: the pair (a, b) of frequency i at position p becomes
+ *   m (a cos t - b sin t), m (b cos t + a sin t),  t = p inv_freq[i],
+ * for i < rot_dim / 2; elements from rot_dim on stay as they are.  inv_freq fp64
+ * [rot_dim / 2] (device, 8-byte aligned; radians a position), magnitude m
+ * finite, rot_dim even, 2 .. head_dim.  t is reduced in fp64; sine, cosine and
+ * the turn are fp32 (sines and cosines within 3e-7 up to positions of 2^24),
+ * results are rounded once.  The turn by -p undoes the turn by p (and, times m,
+ * takes gradients back through it). */
+typedef struct {
+  const double* inv_freq;
+  int32_t rot_dim, layout;
+  float magnitude;
+} loopq_rope_spec;
+
+/* How loopq_rope_frequencies treats contexts `factor` times as long. */
+typedef enum {
+  LOOPQ_ROPE_PLAIN = 0,  /* f_i = base^(-2 i / rot_dim) */
+  LOOPQ_ROPE_LINEAR = 1, /* f_i / factor */
+  LOOPQ_ROPE_BASE = 2,   /* base times factor^(rot_dim / (rot_dim - 2)): the slowest turns by f / factor, the fastest as before */
+  LOOPQ_ROPE_PARTS = 3   /* g f_i + (1 - g) f_i / factor, g = (length f_i / 2 pi - low) / (high - low) within [0, 1]:
+                            what turns over `high` times within the original length stays, what turns less than
+                            `low` times is stretched */
+} loopq_rope_scaling;
+
+/* The frequencies of a scaling as fp64 [rot_dim / 2] in host memory (host only).
+ * base > 1; factor >= 1 (ignored by PLAIN); length > 0 and 0 <= low < high
+ * (PARTS only); all finite.  rot_dim even, 2 .. 128 (from 4 on for BASE). */
+int32_t loopq_rope_frequencies(int32_t scaling, int32_t rot_dim, double base, double factor, double length,
+                               double low, double high, double* inv_freq_host);
+
+/* x, out [tokens][heads][head_dim] in `dtype`, tokens ldx and ldo elements apart,
+ * 16-byte aligned rows; positions int32 [tokens] (any sign).  out may be x itself
+ * (the same address and distance) or, with ldx = ldo, other columns of the same
+ * wider rows.  head_dim 64, 96 or 128; heads * head_dim <= 2^20. */
+int32_t loopq_rope(const void* x, int64_t ldx, int32_t dtype, int32_t tokens, int32_t heads, int32_t head_dim,
+                   const int32_t* positions, const loopq_rope_spec* rope_host, void* out, int64_t ldo, void* stream);
+
+/* loopq_kv_write with rotary positions, and the new tokens' queries: k is turned
+ * and then, with v as it is, rounded to bf16 and written to the slab; q is turned
+ * into q_out.  Token i of the n that cu gives row b (the last of its lens[b]
+ * tokens, see loopq_kv_write) is at position lens[b] - n + i.  cu, k, v, dtype,
+ * tokens as for loopq_kv_write: a token whose position has no page is dropped (its
+ * q is turned all the same).  q [tokens][heads_q][head_dim] in `dtype`, q_out the
+ * same shape in q_dtype (bf16 queries suit loopq_attn_prefill), 16-byte aligned
+ * rows ldq and ldqo elements apart; q_out may be q itself (the same address,
+ * type and distance) or other columns of the same wider rows.  q and q_out may
+ * both be NULL (heads_q is ignored then).  Rows of q_out from cu[rows] on are not
+ * written.  heads_q * head_dim <= 2^20. */
+int32_t loopq_kv_write_rope(const loopq_kv_pool* pool_host, int32_t slab, const loopq_kv_table* table_host,
+                            const int32_t* cu, const loopq_rope_spec* rope_host, const void* k, int64_t ldk,
+                            const void* v, int64_t ldv, int32_t dtype, int32_t tokens, const void* q, int64_t ldq,
+                            int32_t heads_q, void* q_out, int64_t ldqo, int32_t q_dtype, void* stream);
 
 #ifdef __cplusplus
 }
