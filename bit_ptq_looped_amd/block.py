@@ -41,6 +41,8 @@ SIGNATURES = {
     "loopq_rope_frequencies": ([_I, _I, _D, _D, _D, _D, _D, ctypes.POINTER(_D)], _I),
     "loopq_rope": ([_P, _L, _I, _I, _I, _I, _P, _RP, _P, _L, _P], _I),
     "loopq_kv_write_rope": ([kv._PP, _I, kv._TP, _P, _RP, _P, _L, _P, _L, _I, _I, _P, _L, _I, _P, _L, _I, _P], _I),
+    "loopq_adapter_workspace_bytes": ([_I, _I, kv._ZP], _I),
+    "loopq_adapter_apply": ([_P, _L, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _P, _L, _P, _Z, _P], _I),
 }
 
 _lib = None
@@ -93,6 +95,12 @@ def loopq_rope_frequencies(scaling: int, rot_dim: int, base: float = 10000.0, fa
     _check(load().loopq_rope_frequencies(scaling, rot_dim, base, factor, length, low, high, f),
            "loopq_rope_frequencies")
     return list(f)
+
+
+def loopq_adapter_workspace_bytes(rows: int, max_rank: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().loopq_adapter_workspace_bytes(rows, max_rank, _ref(b)), "loopq_adapter_workspace_bytes")
+    return b.value
 
 
 # ----------------------------------------------------------------- device calls
@@ -149,3 +157,31 @@ def loopq_kv_write_rope(pool, slab: int, table: KVTable, cu, rope: Rope, k, v, q
     _check(load().loopq_kv_write_rope(_ref(p), slab, _ref(_table(table)), _ints(cu, "cu", table.lens.numel() + 1),
                                       _ref(_rope(rope)), kp, ldk, vp, ldv, _dtype_code(k), k.shape[0], qp, ldq,
                                       heads_q, op, ldo, q_dtype, _on(k, stream)), "loopq_kv_write_rope")
+
+
+def loopq_adapter_apply(x, ids, A, B, scales, y, workspace, ranks=None, stream=None):
+    """y [rows][N] float32 += scales[a] B[a] (A[a] x) for the adapter a = ids[row] of each row.
+
+    x [rows][K], A bfloat16 [adapters][max_rank][K], B bfloat16 [adapters][N][max_rank]."""
+    torch = loopq._torch_mod()
+    rows, K = x.shape
+    n, rank, width = A.shape
+    if width != K or B.shape[0] != n or B.shape[2] != rank:
+        raise ValueError("A is [adapters][max_rank][K], B [adapters][N][max_rank]")
+    N = B.shape[1]
+    xp, ldx, dtype = _rows2(x, "x", rows, K)
+    yp, ldy, y_dtype = _rows2(y, "y", rows, N)
+    if y_dtype != loopq.LOOPQ_F32:
+        raise ValueError("y must be float32")
+    _check(load().loopq_adapter_apply(xp, ldx, dtype, rows, K, N, _ints(ids, "ids", rows),
+                                      _dense(A, "A", torch.bfloat16, 1), _dense(B, "B", torch.bfloat16, 1),
+                                      _dense(scales, "scales", torch.float32, n),
+                                      _ints(ranks, "ranks", n) if ranks is not None else None, n, rank, yp, ldy,
+                                      *kv._ws(workspace), _on(x, stream)), "loopq_adapter_apply")
+
+
+# ----------------------------------------------------------------- buffer helpers
+
+def empty_adapter_workspace(rows: int, max_rank: int, device="cuda"):
+    import torch
+    return torch.empty(max(loopq_adapter_workspace_bytes(rows, max_rank), 256), dtype=torch.uint8, device=device)

@@ -222,4 +222,52 @@ int32_t loopq_kv_write_rope(const loopq_kv_pool* pool, int32_t slab, const loopq
   return hip_status(launch_rope(a, s));
 }
 
+int32_t loopq_adapter_workspace_bytes(int32_t rows, int32_t max_rank, size_t* bytes) {
+  if (!bytes || rows < 0 || max_rank <= 0) return LOOPQ_ERR_INVALID_ARG;
+  if (max_rank % 8 || max_rank > kAdapterMaxRank) return LOOPQ_ERR_UNSUPPORTED;
+  *bytes = adapter_workspace_bytes(rows, max_rank);
+  return LOOPQ_OK;
+}
+
+int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t rows, int32_t K, int32_t N,
+                            const int32_t* ids, const void* A, const void* B, const float* scales, const int32_t* ranks,
+                            int32_t adapters, int32_t max_rank, float* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (rows < 0 || K <= 0 || N <= 0 || adapters <= 0 || max_rank <= 0) return LOOPQ_ERR_INVALID_ARG;
+  if (!is_dtype(dtype)) return LOOPQ_ERR_UNSUPPORTED;
+  if (K % 8 || K > 65536 || N > (1 << 20) || adapters > (1 << 16)) return LOOPQ_ERR_UNSUPPORTED;
+  if (max_rank % 8 || max_rank > kAdapterMaxRank || rows > kAdapterMaxRows) return LOOPQ_ERR_UNSUPPORTED;
+  if (rows == 0) return LOOPQ_OK;
+  if (!ids || !A || !B || !scales || !y) return LOOPQ_ERR_INVALID_ARG;
+  int32_t st = check_rows(x, ldx, K, rows, dtype);
+  if (st != LOOPQ_OK) return st;
+  if (rows > 1 && ldy < N) return LOOPQ_ERR_INVALID_ARG;
+  if (!aligned(ids, 4) || !aligned(A, 16) || !aligned(B, 16) || !aligned(scales, 4) || !aligned(ranks, 4) || !aligned(y, 4))
+    return LOOPQ_ERR_ALIGNMENT;
+  AdapterArgs a;
+  a.x = x;
+  a.ldx = rows > 1 ? ldx : K;
+  a.x_bf16 = dtype == LOOPQ_BF16;
+  a.rows = rows;
+  a.K = K;
+  a.N = N;
+  a.ids = ids;
+  a.A = reinterpret_cast<const uint16_t*>(A);
+  a.B = reinterpret_cast<const uint16_t*>(B);
+  a.scales = scales;
+  a.ranks = ranks;
+  a.adapters = adapters;
+  a.R = max_rank;
+  a.y = y;
+  a.ldy = rows > 1 ? ldy : N;
+  const int item = item_bytes(dtype);
+  if (share({x, a.ldx * item, (int64_t)K * item}, {y, a.ldy * 4, (int64_t)N * 4}, rows)) return LOOPQ_ERR_INVALID_ARG;
+  st = check_workspace(workspace, workspace_bytes, adapter_workspace_bytes(rows, max_rank));
+  if (st != LOOPQ_OK) return st;
+  a.z = reinterpret_cast<float*>(workspace);
+  hipStream_t s = as_stream(stream);
+  TimingScope ts(LOOPQ_KERNEL_ADAPTER, s);
+  return hip_status(launch_adapter(a, s));
+}
+
 }  // extern "C"

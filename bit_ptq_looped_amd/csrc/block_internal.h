@@ -54,4 +54,23 @@ struct RopeArgs {
 };
 hipError_t launch_rope(RopeArgs a, hipStream_t s);
 
+constexpr int kAdapterMaxRank = 128;
+constexpr int kAdapterMaxRows = 1 << 20;
+struct AdapterArgs {
+  const void* x;
+  int64_t ldx;           // elements
+  int x_bf16, rows, K, N;
+  const int32_t* ids;    // [rows]
+  const uint16_t* A;     // bf16 [adapters][R][K]
+  const uint16_t* B;     // bf16 [adapters][N][R]
+  const float* scales;   // [adapters]
+  const int32_t* ranks;  // [adapters], or null: all R
+  int adapters, R;
+  float* y;
+  int64_t ldy;
+  float* z;              // [rows][R]
+};
+size_t adapter_workspace_bytes(int64_t rows, int max_rank);
+hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
+
 }  // namespace loopq

@@ -451,7 +451,8 @@ typedef enum {
   LOOPQ_KERNEL_ATTN = 7,            /* attention over the paged cache (loopq_kv.h; one record per call) */
   LOOPQ_KERNEL_KV = 8,              /* cache pages: reserve, write, fork, trim, compact, copy (one record per call) */
   LOOPQ_KERNEL_NORM = 9,            /* residual and RMS norm (loopq_block.h) */
-  LOOPQ_KERNEL_ROPE = 10            /* rotary positions, with or without the cache write (loopq_block.h) */
+  LOOPQ_KERNEL_ROPE = 10,           /* rotary positions, with or without the cache write (loopq_block.h) */
+  LOOPQ_KERNEL_ADAPTER = 11         /* low-rank adapters (loopq_block.h; one record per call) */
 } loopq_kernel_id;
 
 /* Turn the hooks on (1) or off (0).  Host only; cheap. */

@@ -2,7 +2,8 @@
  * loopq_block.h -- what a block of a looped transformer needs between its
  * quantized linears (include/loopq.h) and the attention (include/loopq_kv.h),
  * for AMD Instinct MI355X (gfx950): the residual's addition with the
- * root-mean-square norm, and rotary positions.
+ * root-mean-square norm, rotary positions, and low-rank adapters of many
+ * requests beside a shared projection.
  *
  * The conventions of loopq.h hold: device pointers unless the name ends in
  * _host, work is enqueued on `stream` and the call returns, the caller owns
@@ -10,8 +11,8 @@
  * of no rows is a no-op.  Buffers must not overlap unless a call says so.
  * "16-byte aligned rows" means the pointer and, where there is more than one
  * row, the distance from a row to the next; columns of the same wider rows
- * qualify.  Values read from device memory (positions, lengths, page tables)
- * are never trusted with an address.
+ * qualify.  Values read from device memory (ids, ranks, positions, lengths,
+ * page tables) are never trusted with an address.
  */
 #ifndef LOOPQ_BLOCK_H
 #define LOOPQ_BLOCK_H
@@ -113,6 +114,29 @@ int32_t loopq_kv_write_rope(const loopq_kv_pool* pool_host, int32_t slab, const 
                             const int32_t* cu, const loopq_rope_spec* rope_host, const void* k, int64_t ldk,
                             const void* v, int64_t ldv, int32_t dtype, int32_t tokens, const void* q, int64_t ldq,
                             int32_t heads_q, void* q_out, int64_t ldqo, int32_t q_dtype, void* stream);
+
+/* Low-rank adapters of many requests, added to a shared projection's result:
+ *   y_m += scales[a] B_a (A_a x_m),  a = ids[m],
+ * for every row m whose id is an adapter's (0 <= ids[m] < adapters); other rows
+ * of y are neither read nor written.  x [rows][K] in `dtype` (the input of the
+ * linear that wrote y), 16-byte aligned rows ldx elements apart; y fp32
+ * [rows][N], rows ldy elements apart, 4-byte aligned.  A bf16
+ * [adapters][max_rank][K] and B bf16 [adapters][N][max_rank], contiguous, 16-byte
+ * aligned.  ids int32 [rows] in any order (rows of one request side by side cost
+ * least); scales fp32 [adapters]; ranks int32 [adapters] or NULL: adapter a uses
+ * the first ranks[a] (within 0 .. max_rank) rows of A_a and columns of B_a, the rest
+ * is not used, whatever it holds.  ids, scales, ranks: device, 4-byte aligned.
+ * Products of x and A and of A x and B are formed from all bits of their factors,
+ * sums are fp32 in an order that depends on the sizes only (a row's result does
+ * not depend on other rows' ids).  An infinity or NaN in a row or an adapter
+ * reaches no row but its own.
+ * max_rank a multiple of 8 up to 128; K % 8 == 0, K <= 65536; N <= 2^20;
+ * adapters <= 2^16; rows <= 2^20.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank). */
+int32_t loopq_adapter_workspace_bytes(int32_t rows, int32_t max_rank, size_t* bytes_host);
+int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t rows, int32_t K, int32_t N,
+                            const int32_t* ids, const void* A, const void* B, const float* scales,
+                            const int32_t* ranks, int32_t adapters, int32_t max_rank, float* y, int64_t ldy,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

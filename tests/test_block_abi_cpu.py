@@ -183,3 +183,36 @@ def test_frequencies():
         assert p == f if turns >= 32 else p < f
     assert block.loopq_rope_frequencies(block.LOOPQ_ROPE_PARTS, 64, 500000.0, 1.0, 8192.0, 1.0, 4.0) == \
         pytest.approx(block.loopq_rope_frequencies(block.LOOPQ_ROPE_PLAIN, 64, 500000.0), rel=1e-14)
+
+
+# ----------------------------------------------------------------- adapters
+
+def adapter(lib, **kw):
+    f = dict(x=FAKE, ldx=64, dt=F32, rows=5, K=64, N=48, ids=FAKE + MB, A=FAKE + 2 * MB, B=FAKE + 3 * MB, scales=FAKE + 4 * MB,
+             ranks=FAKE + 5 * MB, adapters=3, max_rank=16, y=FAKE + 6 * MB, ldy=48, ws=FAKE + 7 * MB, size=MB, stream=None)
+    f.update(kw)
+    return lib.loopq_adapter_apply(*f.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INVALID), (dict(rows=(1 << 20) + 1), UNSUPPORTED), (dict(K=0), INVALID), (dict(K=60), UNSUPPORTED), (dict(K=65544), UNSUPPORTED),
+    (dict(N=0), INVALID), (dict(N=(1 << 20) + 1), UNSUPPORTED), (dict(adapters=0), INVALID), (dict(adapters=(1 << 16) + 1), UNSUPPORTED),
+    (dict(max_rank=0), INVALID), (dict(max_rank=12), UNSUPPORTED), (dict(max_rank=136), UNSUPPORTED), (dict(dt=2), UNSUPPORTED),
+    (dict(x=None), INVALID), (dict(ids=None), INVALID), (dict(A=None), INVALID), (dict(B=None), INVALID), (dict(scales=None), INVALID),
+    (dict(y=None), INVALID), (dict(ldx=56), INVALID), (dict(ldy=47), INVALID), (dict(x=FAKE + 8), ALIGNMENT), (dict(ldx=66), ALIGNMENT),
+    (dict(ids=FAKE + MB + 2), ALIGNMENT), (dict(A=FAKE + 2 * MB + 8), ALIGNMENT), (dict(B=FAKE + 3 * MB + 8), ALIGNMENT),
+    (dict(scales=FAKE + 4 * MB + 1), ALIGNMENT), (dict(ranks=FAKE + 5 * MB + 2), ALIGNMENT), (dict(y=FAKE + 6 * MB + 2), ALIGNMENT),
+    (dict(y=FAKE), INVALID), (dict(y=FAKE + 256), INVALID), (dict(ws=None), WORKSPACE), (dict(size=0), WORKSPACE), (dict(ws=FAKE + 7 * MB + 64), ALIGNMENT)])
+def test_adapter_arguments(lib, kw, want):
+    assert adapter(lib, **kw) == want
+
+
+def test_adapter_workspace(lib):
+    need = block.loopq_adapter_workspace_bytes(5, 16)
+    assert need % 256 == 0 and need >= 5 * 16 * 4
+    assert adapter(lib, size=need - 1) == WORKSPACE
+    assert adapter(lib, rows=0, x=None, y=None, ws=None) == 0
+    for args, want in (((-1, 16), INVALID), ((5, 0), INVALID), ((5, 12), UNSUPPORTED), ((5, 136), UNSUPPORTED)):
+        with pytest.raises(loopq.LoopQError) as e:
+            block.loopq_adapter_workspace_bytes(*args)
+        assert e.value.status == want
