@@ -138,10 +138,275 @@ hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// --------------------------------------------------------------- many rows
+//
+// Both products on the bf16 MFMA (16x16x32): the adapter's rows are the first
+// operand, the tokens the second, so that a lane holds four consecutive ranks
+// (outputs) of one token, 16 bytes of z (y).  fp32 values enter as three exact
+// bf16 planes, smallest first, so products are exact and sums fp32.  A tile of
+// tokens goes through each adapter that occurs in it, whole, and every token
+// keeps the result of its own: no sorting, no zeros multiplied into other rows
+// (an infinity in one adapter stays with its tokens), and the cost of a mixed
+// tile is its number of adapters, which for prompts is one or two.
+
+constexpr int kTile = 32;    // tokens of a shrink work-group
+constexpr int kChunk = 128;  // K of a step: a lane's 32 consecutive elements
+constexpr int kMaxSplits = 8;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Adapters of a wave's tokens, one after the other: lane l (of `lanes`) holds the
+// id of token l; next() takes the first one left.
+struct Adapters {
+  uint64_t left;
+  int id;
+  __device__ __forceinline__ Adapters(int id_, uint64_t lanes) : left(__ballot(id_ >= 0) & lanes), id(id_) {}
+  __device__ __forceinline__ int next() {
+    const int a = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+    left &= ~__ballot(id == a);
+    return a;
+  }
+};
+
+// z partial sums: work-group (tile, split) of 4 waves; the chunks of K are dealt to
+// splits x 4 waves in runs, the waves' sums added in their order through LDS.
+// RT: rank tiles of 16 (R <= 16 RT).
+template <int BF, int RT>
+__global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
+  constexpr int LD = 16 * RT + 4;
+  __shared__ float sum[4][kTile][LD];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int li = lane & 15, lq = lane >> 4;
+  const int64_t m0 = (int64_t)blockIdx.x * kTile;
+  const int64_t mine = m0 + (lane & 31);
+  const int id = mine < a.rows ? adapter_of(a, mine) : -1;
+  Adapters todo(id, 0xFFFFFFFFull);
+  if (todo.left == 0) return;
+  const int chunks = (a.K + kChunk - 1) / kChunk, parts = gridDim.y * 4, part = blockIdx.y * 4 + wave;
+  const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
+  int ids[2];
+  const char* x[2];
+  constexpr int item = BF ? 2 : 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    ids[h] = __shfl(id, 16 * h + li);
+    const int64_t m = m0 + 16 * h + li;
+    x[h] = reinterpret_cast<const char*>(a.x) + (ids[h] >= 0 ? m : 0) * a.ldx * item;
+  }
+  while (todo.left) {
+    const int ad = todo.next();
+    const int rank = rank_of(a, ad);
+    const uint16_t* A = a.A + (int64_t)ad * a.R * a.K;
+    v4f acc[2][RT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[h][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = c0; c < c1; ++c) {
+      const int k0 = c * kChunk + 32 * lq;
+      u32x4 xr[2][4][BF ? 1 : 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = ids[h] == ad && k0 + 8 * i < a.K;
+#pragma unroll
+          for (int p = 0; p < (BF ? 1 : 2); ++p)
+            xr[h][i][p] = in ? *reinterpret_cast<const u32x4*>(x[h] + (int64_t)(k0 + 8 * i) * item + 16 * p) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x4 w[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int j = 16 * t + li;
+          w[t] = j < rank && k0 + 8 * i < a.K ? *reinterpret_cast<const u32x4*>(A + (int64_t)j * a.K + k0 + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (BF) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[h][t] = s2_mm(w[t], xr[h][i][0], acc[h][t]);
+          } else {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] = __uint_as_float(xr[h][i][0][e]);
+              v[4 + e] = __uint_as_float(xr[h][i][1][e]);
+            }
+            v4u planes[3];
+            planes8(v, planes);
+#pragma unroll
+            for (int p = 2; p >= 0; --p)
+#pragma unroll
+              for (int t = 0; t < RT; ++t) acc[h][t] = s2_mm(w[t], planes[p], acc[h][t]);
+          }
+        }
+      }
+    }
+    mfma_settle_before_join();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (ids[h] == ad) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) *reinterpret_cast<v4f*>(&sum[wave][16 * h + li][16 * t + 4 * lq]) = acc[h][t];
+      }
+  }
+  __syncthreads();
+  float* z = a.z + ((int64_t)blockIdx.y * a.rows + m0) * a.R;
+  for (int i = threadIdx.x; i < kTile * a.R; i += 256) {
+    const int m = i / a.R, j = i - m * a.R;
+    if (m0 + m >= a.rows) continue;
+    const int own = adapter_of(a, m0 + m);
+    if (own < 0 || j >= rank_of(a, own)) continue;
+    float v = sum[0][m][j];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += sum[w][m][j];
+    z[i] = a.scales[own] * v;
+  }
+}
+
+// y += B z: a wave takes 16 tokens and a stripe of N, 64 outputs a step.  RS: steps
+// of 32 ranks (R <= 32 RS).  VEC: rows of y are 16-byte aligned.
+template <int RS, bool VEC>
+__global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int splits, int stripe) {
+  const int lane = threadIdx.x & 63;
+  const int li = lane & 15, lq = lane >> 4;
+  const int64_t m = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 16 + li;
+  const int id = m < a.rows ? adapter_of(a, m) : -1;
+  Adapters todo(id, 0xFFFFull);
+  if (todo.left == 0) return;
+  v4u z[RS][3];
+  const int mine = id >= 0 ? rank_of(a, id) : 0;
+#pragma unroll
+  for (int t = 0; t < RS; ++t) {
+    const int j = 32 * t + 8 * lq;
+    float v[8] = {};
+    if (j < mine) {
+      for (int sp = 0; sp < splits; ++sp) {
+        const v4f* p = reinterpret_cast<const v4f*>(a.z + ((int64_t)sp * a.rows + m) * a.R + j);
+        const v4f u0 = p[0], u1 = p[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += u0[e];
+          v[4 + e] += u1[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j + e < mine ? v[e] : 0.0f;
+    planes8(v, z[t]);
+  }
+  const int n_begin = blockIdx.y * stripe, n_end = min(a.N, n_begin + stripe);
+  float* y = a.y + (id >= 0 ? m : 0) * a.ldy;
+  while (todo.left) {
+    const int ad = todo.next();
+    const int rank = rank_of(a, ad);
+    const uint16_t* B = a.B + (int64_t)ad * a.N * a.R;
+    // which of the lane's eight ranks of a step the adapter has
+    u32x4 keep[RS];
+#pragma unroll
+    for (int t = 0; t < RS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int have = rank - (32 * t + 8 * lq + 2 * e);
+        keep[t][e] = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
+      }
+    for (int n0 = n_begin; n0 < n_end; n0 += 64) {
+      v4f acc[4], old[4];
+      u32x4 b[RS][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 16 * i + li;
+#pragma unroll
+        for (int t = 0; t < RS; ++t) {
+          const int j = 32 * t + 8 * lq;
+          b[t][i] = n < a.N && j < rank ? *reinterpret_cast<const u32x4*>(B + (int64_t)n * a.R + j) & keep[t] : u32x4{0u, 0u, 0u, 0u};
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 16 * i + 4 * lq;
+        if (id != ad) continue;
+        if (VEC && n + 4 <= a.N) {
+          old[i] = *reinterpret_cast<const v4f*>(y + n);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) old[i][e] = n + e < a.N ? y[n + e] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int t = 0; t < RS; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = s2_mm(b[t][i], z[t][p], acc[i]);
+      mfma_settle_before_join();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 16 * i + 4 * lq;
+        if (id != ad) continue;
+        if (VEC && n + 4 <= a.N) {
+          *reinterpret_cast<v4f*>(y + n) = old[i] + acc[i];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) y[n + e] = old[i][e] + acc[i][e];
+        }
+      }
+    }
+  }
+}
+
+int splits_for(int64_t rows, int K) {
+  const int64_t tiles = (rows + kTile - 1) / kTile;
+  const int64_t want = 768 / tiles, most = (K + 4 * kChunk - 1) / (4 * kChunk);
+  const int64_t n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
+}
+
+template <int RT>
+void shrink_tiles(const AdapterArgs& a, dim3 grid, hipStream_t s) {
+  if (a.x_bf16) shrink_tile_kernel<1, RT><<<grid, 256, 0, s>>>(a);
+  else shrink_tile_kernel<0, RT><<<grid, 256, 0, s>>>(a);
+}
+template <int RS>
+void expand_tiles(const AdapterArgs& a, dim3 grid, int splits, int stripe, hipStream_t s) {
+  if (a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0) expand_tile_kernel<RS, true><<<grid, 256, 0, s>>>(a, splits, stripe);
+  else expand_tile_kernel<RS, false><<<grid, 256, 0, s>>>(a, splits, stripe);
+}
+
+hipError_t launch_tiles(const AdapterArgs& a, hipStream_t s) {
+  const int splits = splits_for(a.rows, a.K);
+  const dim3 shrink((a.rows + kTile - 1) / kTile, splits);
+  if (a.R <= 16) shrink_tiles<1>(a, shrink, s);
+  else if (a.R <= 32) shrink_tiles<2>(a, shrink, s);
+  else if (a.R <= 64) shrink_tiles<4>(a, shrink, s);
+  else shrink_tiles<8>(a, shrink, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int groups = (a.rows + 63) / 64, steps = (a.N + 63) / 64;
+  int stripes = (2048 + groups - 1) / groups;
+  if (stripes > steps) stripes = steps;
+  const int stripe = (steps + stripes - 1) / stripes * 64;
+  const dim3 expand(groups, (a.N + stripe - 1) / stripe);
+  if (a.R <= 32) expand_tiles<1>(a, expand, splits, stripe, s);
+  else if (a.R <= 64) expand_tiles<2>(a, expand, splits, stripe, s);
+  else expand_tiles<4>(a, expand, splits, stripe, s);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t adapter_workspace_bytes(int64_t rows, int max_rank) { return (size_t)(rows * max_rank * 4 + 255) / 256 * 256; }
+// z of each split of K (at most what splits_for gives for any K)
+size_t adapter_workspace_bytes(int64_t rows, int max_rank) {
+  return (size_t)(splits_for(rows > 0 ? rows : 1, 1 << 30) * rows * max_rank * 4 + 255) / 256 * 256;
+}
 
-hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s) { return launch_rows(a, s); }
+hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s) {
+  return a.rows <= 64 ? launch_rows(a, s) : launch_tiles(a, s);
+}
 
 }  // namespace loopq
