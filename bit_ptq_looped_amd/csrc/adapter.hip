@@ -150,7 +150,7 @@ hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
 // tile is its number of adapters, which for prompts is one or two.
 
 constexpr int kTile = 32;    // tokens of a shrink work-group
-constexpr int kChunk = 128;  // K of a step: a lane's 32 consecutive elements
+constexpr int kChunk = 128;  // K of a step: four instructions of 64 contiguous bytes a row (of bf16)
 constexpr int kMaxSplits = 8;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -203,16 +203,16 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) acc[h][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int c = c0; c < c1; ++c) {
-      const int k0 = c * kChunk + 32 * lq;
+      const int k0 = c * kChunk + 8 * lq;
       u32x4 xr[2][4][BF ? 1 : 2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool in = ids[h] == ad && k0 + 8 * i < a.K;
+          const bool in = ids[h] == ad && k0 + 32 * i < a.K;
 #pragma unroll
           for (int p = 0; p < (BF ? 1 : 2); ++p)
-            xr[h][i][p] = in ? *reinterpret_cast<const u32x4*>(x[h] + (int64_t)(k0 + 8 * i) * item + 16 * p) : u32x4{0u, 0u, 0u, 0u};
+            xr[h][i][p] = in ? *reinterpret_cast<const u32x4*>(x[h] + (int64_t)(k0 + 32 * i) * item + 16 * p) : u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           const int j = 16 * t + li;
-          w[t] = j < rank && k0 + 8 * i < a.K ? *reinterpret_cast<const u32x4*>(A + (int64_t)j * a.K + k0 + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+          w[t] = j < rank && k0 + 32 * i < a.K ? *reinterpret_cast<const u32x4*>(A + (int64_t)j * a.K + k0 + 32 * i) : u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -110,7 +110,6 @@ int32_t loopq_rms_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* 
   a.ldr = ldr;
   a.lds = lds;
   a.ldy = ldy;
-  a.row0 = 0;
   a.rows = rows;
   a.K = K;
   a.x_bf16 = x_dtype == LOOPQ_BF16;
@@ -118,6 +117,7 @@ int32_t loopq_rms_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* 
   a.y_bf16 = y && y_dtype == LOOPQ_BF16;
   a.per_token = per_token != 0;
   a.eps = eps;
+  a.inv_k = 1.0 / K;
   a.clip = codes ? clip : 1.0f;
   a.qmax = codes && bits_a == 4 ? 7.0f : 127.0f;
   hipStream_t s = as_stream(stream);

@@ -19,12 +19,13 @@ struct NormArgs {
   float* steps;
   int64_t ldx, ldr, lds, ldy;  // elements
   int64_t row0;       // first row of the launch
-  int rows, K;        // rows: all of the call's
+  int rows, K;
   int x_bf16, res_bf16, y_bf16;
   int per_token;
   float eps, clip, qmax;
+  double inv_k;       // 1 / K
 };
-hipError_t launch_rms_norm(NormArgs a, hipStream_t s);
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 
 // One tensor of a rotary call: [tokens][heads][dim], heads side by side.
 struct RopePart {
