@@ -242,6 +242,8 @@ int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t r
   int32_t st = check_rows(x, ldx, K, rows, dtype);
   if (st != LOOPQ_OK) return st;
   if (rows > 1 && ldy < N) return LOOPQ_ERR_INVALID_ARG;
+  // a tile of 32 rows lies within 2^31 bytes
+  if (rows > 1 && (ldx >= kAdapterMaxLd || ldy >= kAdapterMaxLd)) return LOOPQ_ERR_UNSUPPORTED;
   if (!aligned(ids, 4) || !aligned(A, 16) || !aligned(B, 16) || !aligned(scales, 4) || !aligned(ranks, 4) || !aligned(y, 4))
     return LOOPQ_ERR_ALIGNMENT;
   AdapterArgs a;

@@ -57,6 +57,7 @@ hipError_t launch_rope(RopeArgs a, hipStream_t s);
 
 constexpr int kAdapterMaxRank = 128;
 constexpr int kAdapterMaxRows = 1 << 20;
+constexpr int64_t kAdapterMaxLd = 1 << 24;  // 32 rows of fp32 stay below 2^31 bytes
 struct AdapterArgs {
   const void* x;
   int64_t ldx;           // elements
