@@ -148,22 +148,35 @@ hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
 
 // --------------------------------------------------------------- many rows
 //
-// Both products on the bf16 MFMA (16x16x32): the adapter's rows are the first
-// operand, the tokens the second, so that a lane holds four consecutive ranks
-// (outputs) of one token, 16 bytes of z (y).  fp32 values enter as three exact
-// bf16 planes, smallest first, so products are exact and sums fp32.  A tile of
-// tokens goes through each adapter that occurs in it, whole, and every token
-// keeps the result of its own: no sorting, no zeros multiplied into other rows
-// (an infinity in one adapter stays with its tokens), and the cost of a mixed
-// tile is its number of adapters, which for prompts is one or two.
+// Both products on the bf16 MFMA.  fp32 values enter as three exact bf16 planes,
+// smallest first, so products are exact and sums fp32.  A tile of tokens goes
+// through each adapter that occurs in it, whole, and every token keeps the result
+// of its own: no sorting, no zeros multiplied into other rows (an infinity in one
+// adapter stays with its tokens), and a tile costs its number of adapters, which for
+// prompts is one or two.
+//
+// An MFMA operand wants neighbouring lanes in different rows, memory wants them side
+// by side: four lanes in four rows take four times the address cycles.  So what a
+// work-group shares goes through LDS, and y is read and written an element a lane,
+// 32 side by side.  A tile of more than kFew adapters (a batch of single tokens)
+// goes without LDS: its waves take the adapters of their own tokens one by one,
+// operands straight from memory.  The products and sums of a token are the same,
+// in the same order, either way.
 
-constexpr int kTile = 32;  // tokens of a shrink work-group
+constexpr int kTile = 64;    // tokens of a shrink work-group, 16 a wave
+constexpr int kTokens = 128; // tokens of an expand work-group, 32 a wave
+constexpr int kFew = 6;
 constexpr int kMaxSplits = 8;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
-// Adapters of a wave's tokens, one after the other: lane l (of `lanes`) holds the
-// id of token l; next() takes the first one left.
+__device__ __forceinline__ v16f mm32(const u32x4& a, const u32x4& b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// Adapters of up to 64 tokens, one after the other: lane l holds the id of token l;
+// next() takes the first one left.
 struct Adapters {
   uint64_t left;
   int id;
@@ -173,14 +186,8 @@ struct Adapters {
     left &= ~__ballot(id == a);
     return a;
   }
+  __device__ __forceinline__ int next_or_none() { return left ? next() : -1; }
 };
-
-// How many adapters occur.
-__device__ __forceinline__ int count_of(Adapters all) {
-  int n = 0;
-  for (; all.left; ++n) all.next();
-  return n;
-}
 
 // Loads and stores go through buffer resources of less than 2^31 bytes, so that a
 // lane without a part in one names the place kNone, past the end: the load gives 0
@@ -193,275 +200,358 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
 }
 
-// z partial sums: work-group (tile, split) of 4 waves.  K is cut into steps of KS
-// MFMA (32 KS elements), the split's steps into four runs, whose sums are added in
-// their order through LDS: a wave takes one run of every adapter or, in a tile of
-// more than kFew adapters, the four runs of every fourth adapter (the sums are the
-// same).  Two sets of registers: the next step is loaded while one is multiplied.
-// RT: rank tiles of 16 (R <= 16 RT).
-constexpr int kFew = 4;
+// acc[t] += A x of 32 elements of K: RT rank tiles of 16, 16 tokens
+template <int BF, int RT>
+__device__ __forceinline__ void shrink_mm(const u32x4 (&w)[RT], const u32x4 (&x)[BF ? 1 : 2], v4f (&acc)[RT]) {
+  if constexpr (BF) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = s2_mm(w[t], x[0], acc[t]);
+  } else {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __uint_as_float(x[0][e]);
+      v[4 + e] = __uint_as_float(x[1][e]);
+    }
+    v4u planes[3];
+    planes8(v, planes);
+#pragma unroll
+    for (int p = 2; p >= 0; --p)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[t] = s2_mm(w[t], planes[p], acc[t]);
+  }
+}
 
-template <int BF, int RT, int KS>
+// z partial sums (16x16x32 MFMA, ranks the first operand, tokens the second: a lane
+// ends with four ranks of a token): work-group (tile of 64 tokens, split of K), 16
+// tokens a wave.  K goes in chunks of 256 bytes a row of x.
+// RT: rank tiles of 16 (R <= 16 RT).
+template <int BF, int RT>
 __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
-  constexpr int LD = 16 * RT + 4;
-  __shared__ float sum[4][kTile][LD];
+  constexpr int item = BF ? 2 : 4;
+  constexpr int KC = 256 / item;         // elements of a chunk
+  constexpr int XS = 256 + 16;           // bytes of a row in LDS: 16 spread the rows over the banks
+  constexpr int WS = KC * 2 + 16;
+  constexpr int WL = KC / 8;             // lanes of a row of A
+  constexpr int WN = (16 * RT * WL + 255) / 256;
+  __shared__ __attribute__((aligned(16))) char sx[kTile * XS];
+  __shared__ __attribute__((aligned(16))) char sw[16 * RT * WS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int64_t m0 = (int64_t)blockIdx.x * kTile;
-  const int64_t mine = m0 + (lane & 31);
-  const int id = mine < a.rows ? adapter_of(a, mine) : -1;
-  Adapters todo(id, 0xFFFFFFFFull);
+  const int id = m0 + lane < a.rows ? adapter_of(a, m0 + lane) : -1;
+  Adapters todo(id, ~0ull);
   if (todo.left == 0) return;
-  const bool mixed = count_of(todo) > kFew;
-  const int steps = (a.K + 32 * KS - 1) / (32 * KS);
-  int first[5];  // of each run, and the end (K <= 65536 and splits <= 8: 32 bits do)
-#pragma unroll
-  for (int r = 0; r < 5; ++r) first[r] = (uint32_t)steps * (blockIdx.y * 4 + r) / (gridDim.y * 4);
-  const int c0 = mixed ? first[0] : wave == 0 ? first[0] : wave == 1 ? first[1] : wave == 2 ? first[2] : first[3];
-  const int c1 = mixed ? first[4] : wave == 0 ? first[1] : wave == 1 ? first[2] : wave == 2 ? first[3] : first[4];
-  constexpr int item = BF ? 2 : 4;
+  int few = 0;
+  for (Adapters all = todo; all.left && few <= kFew; ++few) all.next();
+  const int chunks = (a.K + KC - 1) / KC;
+  const int c0 = (uint32_t)chunks * blockIdx.y / gridDim.y, c1 = (uint32_t)chunks * (blockIdx.y + 1) / gridDim.y;
   const auto xr = resource(reinterpret_cast<const char*>(a.x) + m0 * a.ldx * item, (kTile - 1) * a.ldx * item + a.K * item);
-  int ids[2];
-  uint32_t xat[2];
+  const int my_id = __shfl(id, 16 * wave + li);  // the token of this lane's results
+  float* z = a.z + ((int64_t)blockIdx.y * a.rows + m0 + 16 * wave + li) * a.R;
+  v4f acc[RT];
+  auto finish = [&](int ad, int rank) {
+    mfma_settle_before_join();
+    if (my_id != ad) return;
+    const float s = a.scales[ad];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    ids[h] = __shfl(id, 16 * h + li);
-    xat[h] = (uint32_t)((16 * h + li) * a.ldx * item);
-  }
-  // this wave's adapters: all, or every fourth
-  int skip = mixed ? wave : 0;
-  auto next_adapter = [&]() {
-    for (; todo.left && skip > 0; --skip) todo.next();
-    if (mixed) skip = 3;
-    return todo.left ? todo.next() : -1;
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * t + 4 * lq + e < rank) z[16 * t + 4 * lq + e] = s * acc[t][e];
   };
+  auto clear = [&]() {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+
+  if (few <= kFew) {
+    int xid[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xid[i] = __shfl(id, (int)(threadIdx.x >> 4) + 16 * i);
+    while (todo.left) {
+      const int ad = todo.next(), rank = wave_rank_of(a, ad);
+      const auto wr = resource(a.A + (int64_t)ad * a.R * a.K, (int64_t)rank * a.K * 2);  // rows from the rank on lie outside
+      u32x4 x[4], w[WN];
+      auto load = [&](int c) {
+        const int kx = c * KC + (int)(threadIdx.x & 15) * (16 / item);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = load16(xr, xid[i] == ad && kx < a.K ? (uint32_t)((((int)(threadIdx.x >> 4) + 16 * i) * a.ldx + kx) * item) : kNone);
+        const int kw = c * KC + (int)(threadIdx.x % WL) * 8;
+#pragma unroll
+        for (int i = 0; i < WN; ++i) {
+          const int j = (int)threadIdx.x / WL + i * (256 / WL);
+          w[i] = load16(wr, kw < a.K ? (uint32_t)((j * a.K + kw) * 2) : kNone);
+        }
+      };
+      clear();
+      load(c0);
+      for (int c = c0; c < c1; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(sx + ((int)(threadIdx.x >> 4) + 16 * i) * XS + (threadIdx.x & 15) * 16) = x[i];
+#pragma unroll
+        for (int i = 0; i < WN; ++i) {
+          const int j = (int)threadIdx.x / WL + i * (256 / WL);
+          if (16 * RT * WL >= 256 || j < 16 * RT) *reinterpret_cast<u32x4*>(sw + j * WS + (threadIdx.x % WL) * 16) = w[i];
+        }
+        __syncthreads();
+        if (c + 1 < c1) load(c + 1);
+#pragma unroll
+        for (int s = 0; s < KC / 32; ++s) {
+          u32x4 xo[BF ? 1 : 2], wo[RT];
+#pragma unroll
+          for (int p = 0; p < (BF ? 1 : 2); ++p)
+            xo[p] = *reinterpret_cast<const u32x4*>(sx + (16 * wave + li) * XS + (32 * s + 8 * lq) * item + 16 * p);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) wo[t] = *reinterpret_cast<const u32x4*>(sw + (16 * t + li) * WS + (32 * s + 8 * lq) * 2);
+          shrink_mm<BF, RT>(wo, xo, acc);
+        }
+      }
+      finish(ad, rank);
+    }
+    return;
+  }
+
+  // many adapters: a wave for itself, two sets of registers, KS MFMA steps each
+  constexpr int KS = RT == 1 ? 4 : RT <= 4 ? 2 : 1;
   struct Step {
-    u32x4 x[KS][2][BF ? 1 : 2];
+    u32x4 x[KS][BF ? 1 : 2];
     u32x4 w[KS][RT];
   };
+  Adapters own(my_id, 0xFFFFull);
+  const uint32_t xat = (uint32_t)((16 * wave + li) * a.ldx * item);
+  const int k_end = min(a.K, c1 * KC);
   // always the same number of loads, so that the wait for one step leaves the next one's under way
-  auto load = [&](Step& s, int ad, int rank, int c) {
-    const auto wr = resource(a.A + (int64_t)max(ad, 0) * a.R * a.K, ad < 0 ? 0 : (int64_t)rank * a.K * 2);  // rows from the rank on lie outside
+  auto load = [&](Step& s, int ad, int rank, int k0) {
+    const auto wr = resource(a.A + (int64_t)max(ad, 0) * a.R * a.K, ad < 0 ? 0 : (int64_t)rank * a.K * 2);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-      const int k = (c * KS + i) * 32 + 8 * lq;
-      const bool in = k < a.K;
+      const int k = k0 + 32 * i + 8 * lq;
+      const bool in = k < k_end;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = in && ad >= 0 && ids[h] == ad ? xat[h] + (uint32_t)(k * item) : kNone;
-#pragma unroll
-        for (int p = 0; p < (BF ? 1 : 2); ++p) s.x[i][h][p] = load16(xr, at + 16 * p);
-      }
+      for (int p = 0; p < (BF ? 1 : 2); ++p)
+        s.x[i][p] = load16(xr, in && ad >= 0 && my_id == ad ? xat + (uint32_t)(k * item + 16 * p) : kNone);
 #pragma unroll
       for (int t = 0; t < RT; ++t) s.w[i][t] = load16(wr, in ? (uint32_t)(((16 * t + li) * a.K + k) * 2) : kNone);
     }
   };
-  v4f acc[2][RT];
-  auto multiply = [&](const Step& s, int ad, int c) {
-    int run = wave, begin = c0, end = c1;
-    if (mixed) {
-      run = c < first[1] ? 0 : c < first[2] ? 1 : c < first[3] ? 2 : 3;
-      begin = c < first[1] ? first[0] : c < first[2] ? first[1] : c < first[3] ? first[2] : first[3];
-      end = c < first[1] ? first[1] : c < first[2] ? first[2] : c < first[3] ? first[3] : first[4];
-    }
-    if (c == begin) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[h][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (BF) {
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[h][t] = s2_mm(s.w[i][t], s.x[i][h][0], acc[h][t]);
-        } else {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = __uint_as_float(s.x[i][h][0][e]);
-            v[4 + e] = __uint_as_float(s.x[i][h][1][e]);
-          }
-          v4u planes[3];
-          planes8(v, planes);
-#pragma unroll
-          for (int p = 2; p >= 0; --p)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) acc[h][t] = s2_mm(s.w[i][t], planes[p], acc[h][t]);
-        }
-      }
-    if (c + 1 < end) return;
-    mfma_settle_before_join();
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (ids[h] == ad) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) *reinterpret_cast<v4f*>(&sum[run][16 * h + li][16 * t + 4 * lq]) = acc[h][t];
-      }
+  int ad = own.next_or_none(), k0 = c0 * KC;
+  if (ad < 0 || c0 >= c1) return;
+  int rank = wave_rank_of(a, ad);
+  auto advance = [&]() {
+    if ((k0 += 32 * KS) < k_end) return;
+    ad = own.next_or_none();
+    if (ad >= 0) rank = wave_rank_of(a, ad);
+    k0 = c0 * KC;
   };
-  int ad = c0 < c1 ? next_adapter() : -1;
-  if (ad >= 0) {
-    int rank = wave_rank_of(a, ad), c = c0;
-    auto advance = [&]() {
-      if (++c < c1) return;
-      ad = next_adapter();
-      if (ad >= 0) rank = wave_rank_of(a, ad);
-      c = c0;
-    };
-    Step s0, s1;
-    load(s0, ad, rank, c);
-    for (;;) {
-      int at = c, of = ad;
-      advance();
-      load(s1, ad, rank, c);
-      multiply(s0, of, at);
-      if (ad < 0) break;
-      at = c, of = ad;
-      advance();
-      load(s0, ad, rank, c);
-      multiply(s1, of, at);
-      if (ad < 0) break;
-    }
-  }
-  __syncthreads();
-  float* z = a.z + ((int64_t)blockIdx.y * a.rows + m0) * a.R;
-  for (int i = threadIdx.x; i < kTile * a.R; i += 256) {
-    const int m = i / a.R, j = i - m * a.R;
-    if (m0 + m >= a.rows) continue;
-    const int own = adapter_of(a, m0 + m);
-    if (own < 0 || j >= rank_of(a, own)) continue;
-    float v = 0.0f;
+  auto multiply = [&](const Step& s, int of, int of_rank, int at) {
+    if (at == c0 * KC) clear();
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-      if (first[w] < first[w + 1]) v += sum[w][m][j];
-    z[i] = a.scales[own] * v;
+    for (int i = 0; i < KS; ++i) shrink_mm<BF, RT>(s.w[i], s.x[i], acc);
+    if (at + 32 * KS >= k_end) finish(of, of_rank);
+  };
+  Step s0, s1;
+  load(s0, ad, rank, k0);
+  for (;;) {
+    int at = k0, of = ad, of_rank = rank;
+    advance();
+    load(s1, ad, rank, k0);
+    multiply(s0, of, of_rank, at);
+    if (ad < 0) break;
+    at = k0, of = ad, of_rank = rank;
+    advance();
+    load(s0, ad, rank, k0);
+    multiply(s1, of, of_rank, at);
+    if (ad < 0) break;
   }
 }
 
-// y += B z: a wave takes 16 tokens and a stripe of N, 64 outputs a step; the four
-// waves of a work-group lie side by side in N.  Two sets of registers: the next
-// (adapter, step) is loaded while one is multiplied.  RS: steps of 32 ranks
-// (R <= 32 RS).  VEC: y in 16-byte accesses (aligned rows, N % 4 == 0).
-template <int RS, bool VEC>
+// y += B z (32x32x16 MFMA, tokens the first operand, outputs the second: a lane ends
+// with 16 tokens of one output): work-group (128 tokens, stripe of N), 32 tokens a
+// wave.  NB outputs of B go through LDS at a time; the next ones and the y of the next
+// 32 are loaded while some are multiplied.  RS: steps of 16 ranks (R <= 16 RS).
+template <int RS>
 __global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int splits, int stripe, int stripes) {
+  constexpr int NB = 64;                 // outputs of a block
+  constexpr int BS = 32 * RS + 16;       // bytes of a row of B in LDS
+  constexpr int BL = 2 * RS;             // lanes of a row
+  constexpr int BN = NB * BL / 256;      // loads of a thread
+  static_assert(NB * BL % 256 == 0 || NB * BL == 128, "a block is whole loads of the work-group");
+  __shared__ __attribute__((aligned(16))) char sb[NB * BS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int li = lane & 15, lq = lane >> 4;
+  const int li = lane & 31, lh = lane >> 5;
   const int group = blockIdx.x / stripes;
-  const int64_t m = (int64_t)group * 16 + li;
-  const int id = m < a.rows ? adapter_of(a, m) : -1;
-  Adapters todo(id, 0xFFFFull);
-  if (todo.left == 0) return;
-  const int n_begin = (blockIdx.x - group * stripes) * stripe + 64 * wave;
-  const int n_end = min(a.N, (blockIdx.x - group * stripes) * stripe + stripe);
-  if (n_begin >= n_end) return;
-  const auto yr = resource(a.y + (int64_t)group * 16 * a.ldy, 15 * a.ldy * 4 + (int64_t)a.N * 4);
-  const uint32_t yat = (uint32_t)(li * a.ldy * 4);
-  struct Step {
-    v4f old[4];
-    u32x4 b[RS][4];
-  };
-  // always the same number of loads, so that the wait for one step leaves the next one's under way
-  auto load = [&](Step& s, int ad, int rank, int n0) {
-    const auto br = resource(a.B + (int64_t)max(ad, 0) * a.N * a.R, ad < 0 ? 0 : (int64_t)a.N * a.R * 2);  // outputs from N on lie outside
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + 16 * i + li;
-#pragma unroll
-      for (int t = 0; t < RS; ++t) {
-        const int j = 32 * t + 8 * lq;
-        s.b[t][i] = load16(br, j < rank ? (uint32_t)((n * a.R + j) * 2) : kNone);
-      }
+  const int64_t t0 = (int64_t)group * kTokens;
+  // ids of all the tokens (two a lane) decide the form, those of this wave's 32 the work
+  const int id_a = t0 + lane < a.rows ? adapter_of(a, t0 + lane) : -1;
+  const int id_b = t0 + 64 + lane < a.rows ? adapter_of(a, t0 + 64 + lane) : -1;
+  const int64_t m0 = t0 + 32 * wave;
+  const int id = __shfl(wave < 2 ? id_a : id_b, 32 * (wave & 1) + li);
+  Adapters lower(id_a, ~0ull), upper(id_b, ~0ull);
+  if (lower.left == 0 && upper.left == 0) return;
+  int few = 0;
+  {
+    Adapters l = lower, u = upper;
+    for (; l.left && few <= kFew; ++few) {
+      const int ad = l.next();
+      u.left &= ~__ballot(u.id == ad);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + 16 * i + 4 * lq;
-      if constexpr (VEC) {
-        s.old[i] = __builtin_bit_cast(v4f, load16(yr, id == ad && ad >= 0 && n < a.N ? yat + 4u * n : kNone));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s.old[i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, id == ad && ad >= 0 && n + e < a.N ? yat + 4u * (n + e) : kNone, 0, 0));
-      }
-    }
-  };
-  int ad = todo.next(), rank = wave_rank_of(a, ad), n0 = n_begin;
-  Step s0, s1;
-  load(s0, ad, rank, n0);
-  v4u z[RS][3];
-  const int mine = id >= 0 ? rank_of(a, id) : 0;
-#pragma unroll
-  for (int t = 0; t < RS; ++t) {
-    const int j = 32 * t + 8 * lq;
-    float v[8] = {};
-    if (j < mine) {
-      for (int sp = 0; sp < splits; ++sp) {
-        const v4f* p = reinterpret_cast<const v4f*>(a.z + ((int64_t)sp * a.rows + m) * a.R + j);
-        const v4f u0 = p[0], u1 = p[1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] += u0[e];
-          v[4 + e] += u1[e];
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = j + e < mine ? v[e] : 0.0f;
-    planes8(v, z[t]);
+    for (; u.left && few <= kFew; ++few) u.next();
   }
-  auto multiply = [&](Step& s, int of, int of_rank, int at) {
-    if (of_rank & 7) {  // a lane may have read ranks that the adapter does not have
+  const int n_begin = (blockIdx.x - group * stripes) * stripe, n_end = min(a.N, n_begin + stripe);
+  const auto yr = resource(a.y + m0 * a.ldy, 31 * a.ldy * 4 + (int64_t)a.N * 4);
+  u32x4 z[RS][3];
+  {
+    const int mine = id >= 0 ? rank_of(a, id) : 0;
 #pragma unroll
-      for (int t = 0; t < RS; ++t)
+    for (int t = 0; t < RS; ++t) {
+      const int j = 16 * t + 8 * lh;
+      float v[8] = {};
+      if (j < mine) {
+        for (int sp = 0; sp < splits; ++sp) {
+          const v4f* p = reinterpret_cast<const v4f*>(a.z + ((int64_t)sp * a.rows + m0 + li) * a.R + j);
+          const v4f u0 = p[0], u1 = p[1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int have = of_rank - (32 * t + 8 * lq + 2 * e);
-          const uint32_t keep = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s.b[t][i][e] &= keep;
+          for (int e = 0; e < 4; ++e) {
+            v[e] += u0[e];
+            v[4 + e] += u1[e];
+          }
         }
-    }
-    v4f acc[4];
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int e = 0; e < 8; ++e) v[e] = j + e < mine ? v[e] : 0.0f;
+      v4u planes[3];
+      planes8(v, planes);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) z[t][p] = planes[p];
+    }
+  }
+  // element e of a result is token 8 (e / 4) + 4 lh + e % 4, output li
+  uint32_t mine_of = 0;  // the adapter's tokens among this lane's
+  auto y_at = [&](int e, int n) {
+    const int tok = 8 * (e / 4) + 4 * lh + e % 4;
+    return (mine_of >> e & 1) && n < n_end ? (uint32_t)((tok * a.ldy + n) * 4) : kNone;
+  };
+  auto set_mine = [&](int ad) {
+    mine_of = 0;
+    const uint64_t is = __ballot(ad >= 0 && id == ad);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mine_of |= (uint32_t)(is >> (8 * (e / 4) + 4 * lh + e % 4) & 1) << e;
+  };
+  auto load_y = [&](v16f& old, int n) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, y_at(e, n + li), 0, 0));
+  };
+  // ranks that an adapter does not have among a lane's eight of step t
+  auto cut = [&](u32x4 v, int t, int rank) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int have = rank - (16 * t + 8 * lh + 2 * e);
+      v[e] &= have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
+    }
+    return v;
+  };
+  auto multiply = [&](const u32x4 (&b)[RS], const v16f& old, int n) {
+    v16f acc = {};
 #pragma unroll
     for (int p = 2; p >= 0; --p)
 #pragma unroll
-      for (int t = 0; t < RS; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = s2_mm(s.b[t][i], z[t][p], acc[i]);
+      for (int t = 0; t < RS; ++t) acc = mm32(z[t][p], b[t], acc);
     mfma_settle_before_join();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = at + 16 * i + 4 * lq;
-      const v4f v = s.old[i] + acc[i];
-      if constexpr (VEC) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), yr, id == of && n < a.N ? yat + 4u * n : kNone, 0, 0);
+    for (int e = 0; e < 16; ++e)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + acc[e]), yr, y_at(e, n + li), 0, 0);
+  };
+
+  if (few <= kFew) {
+    while (lower.left || upper.left) {
+      int ad;
+      if (lower.left) {
+        ad = lower.next();
+        upper.left &= ~__ballot(upper.id == ad);
       } else {
+        ad = upper.next();
+      }
+      const int rank = wave_rank_of(a, ad);
+      set_mine(ad);
+      const bool any = __ballot(id == ad) != 0;
+      const auto br = resource(a.B + (int64_t)ad * a.N * a.R, (int64_t)a.N * a.R * 2);  // outputs from N on lie outside
+      u32x4 b[BN > 0 ? BN : 1];
+      auto load_b = [&](int n0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), yr, id == of && n + e < a.N ? yat + 4u * (n + e) : kNone, 0, 0);
+        for (int i = 0; i < (BN > 0 ? BN : 1); ++i) {
+          const int n = (int)threadIdx.x / BL + i * (256 / BL), j = (int)(threadIdx.x % BL) * 8;
+          b[i] = load16(br, j < rank ? (uint32_t)(((n0 + n) * a.R + j) * 2) : kNone);
+        }
+      };
+      v16f old[2];
+      load_b(n_begin);
+      if (any) load_y(old[0], n_begin);
+      for (int n0 = n_begin; n0 < n_end; n0 += NB) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < (BN > 0 ? BN : 1); ++i) {
+          const int n = (int)threadIdx.x / BL + i * (256 / BL);
+          if (BN > 0 || n < NB) *reinterpret_cast<u32x4*>(sb + n * BS + (threadIdx.x % BL) * 16) = b[i];
+        }
+        __syncthreads();
+        if (n0 + NB < n_end) load_b(n0 + NB);
+        if (!any) continue;
+#pragma unroll
+        for (int h = 0; h < NB / 32; ++h) {
+          load_y(old[(h + 1) & 1], n0 + 32 * (h + 1));
+          u32x4 bo[RS];
+#pragma unroll
+          for (int t = 0; t < RS; ++t) {
+            bo[t] = *reinterpret_cast<const u32x4*>(sb + (32 * h + li) * BS + (16 * t + 8 * lh) * 2);
+            if (rank & 7) bo[t] = cut(bo[t], t, rank);
+          }
+          multiply(bo, old[h & 1], n0 + 32 * h);
+        }
       }
     }
+    return;
+  }
+
+  // many adapters: a wave for itself
+  Adapters own(id, 0xFFFFFFFFull);
+  int ad = own.next_or_none();
+  if (ad < 0) return;
+  auto load_own = [&](u32x4 (&b)[RS], int of, int rank, int n) {
+    const auto br = resource(a.B + (int64_t)max(of, 0) * a.N * a.R, of < 0 ? 0 : (int64_t)a.N * a.R * 2);
+#pragma unroll
+    for (int t = 0; t < RS; ++t) {
+      const int j = 16 * t + 8 * lh;
+      b[t] = load16(br, j < rank ? (uint32_t)(((n + li) * a.R + j) * 2) : kNone);
+    }
   };
-  auto advance = [&]() {
-    if ((n0 += 256) < n_end) return;
-    ad = todo.left ? todo.next() : -1;
-    if (ad >= 0) rank = wave_rank_of(a, ad);
-    n0 = n_begin;
-  };
-  for (;;) {
-    int at = n0, of = ad, of_rank = rank;
-    advance();
-    load(s1, ad, rank, n0);
-    multiply(s0, of, of_rank, at);
-    if (ad < 0) break;
-    at = n0, of = ad, of_rank = rank;
-    advance();
-    load(s0, ad, rank, n0);
-    multiply(s1, of, of_rank, at);
-    if (ad < 0) break;
+  while (ad >= 0) {
+    const int rank = wave_rank_of(a, ad);
+    set_mine(ad);
+    u32x4 b0[RS], b1[RS];
+    v16f y0, y1;
+    load_own(b0, ad, rank, n_begin);
+    load_y(y0, n_begin);
+    for (int n = n_begin; n < n_end; n += 64) {
+      load_own(b1, ad, rank, n + 32);
+      load_y(y1, n + 32);
+      if (rank & 7) {
+#pragma unroll
+        for (int t = 0; t < RS; ++t) b0[t] = cut(b0[t], t, rank);
+      }
+      multiply(b0, y0, n);
+      if (n + 32 >= n_end) break;
+      load_own(b0, ad, rank, n + 64);
+      load_y(y0, n + 64);
+      if (rank & 7) {
+#pragma unroll
+        for (int t = 0; t < RS; ++t) b1[t] = cut(b1[t], t, rank);
+      }
+      multiply(b1, y1, n + 32);
+    }
+    ad = own.next_or_none();
   }
 }
 
@@ -472,37 +562,31 @@ int splits_for(int64_t rows, int K) {
   return (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
 
-// KS: what two steps' registers leave room for two or three waves a SIMD
-template <int RT, int KS_BF, int KS_F32>
+template <int RT>
 void shrink_tiles(const AdapterArgs& a, dim3 grid, hipStream_t s) {
-  if (a.x_bf16) shrink_tile_kernel<1, RT, KS_BF><<<grid, 256, 0, s>>>(a);
-  else shrink_tile_kernel<0, RT, KS_F32><<<grid, 256, 0, s>>>(a);
-}
-template <int RS>
-void expand_tiles(const AdapterArgs& a, int grid, int splits, int stripe, int stripes, hipStream_t s) {
-  if (a.ldy % 4 == 0 && a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0)
-    expand_tile_kernel<RS, true><<<grid, 256, 0, s>>>(a, splits, stripe, stripes);
-  else
-    expand_tile_kernel<RS, false><<<grid, 256, 0, s>>>(a, splits, stripe, stripes);
+  if (a.x_bf16) shrink_tile_kernel<1, RT><<<grid, 256, 0, s>>>(a);
+  else shrink_tile_kernel<0, RT><<<grid, 256, 0, s>>>(a);
 }
 
 hipError_t launch_tiles(const AdapterArgs& a, hipStream_t s) {
   const int splits = splits_for(a.rows, a.K);
   const dim3 shrink((a.rows + kTile - 1) / kTile, splits);
-  if (a.R <= 16) shrink_tiles<1, 4, 2>(a, shrink, s);
-  else if (a.R <= 32) shrink_tiles<2, 4, 2>(a, shrink, s);
-  else if (a.R <= 64) shrink_tiles<4, 2, 2>(a, shrink, s);
-  else shrink_tiles<8, 1, 1>(a, shrink, s);
+  if (a.R <= 16) shrink_tiles<1>(a, shrink, s);
+  else if (a.R <= 32) shrink_tiles<2>(a, shrink, s);
+  else if (a.R <= 64) shrink_tiles<4>(a, shrink, s);
+  else shrink_tiles<8>(a, shrink, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int groups = (a.rows + 15) / 16, steps = (a.N + 255) / 256;
-  int stripes = (2048 + groups - 1) / groups;
-  if (stripes > steps) stripes = steps;
-  const int stripe = (steps + stripes - 1) / stripes * 256;
+  const int groups = (a.rows + kTokens - 1) / kTokens, blocks = (a.N + 63) / 64;
+  int stripes = (1536 + groups - 1) / groups;
+  if (stripes > blocks) stripes = blocks;
+  const int stripe = (blocks + stripes - 1) / stripes * 64;
   stripes = (a.N + stripe - 1) / stripe;
-  if (a.R <= 32) expand_tiles<1>(a, groups * stripes, splits, stripe, stripes, s);
-  else if (a.R <= 64) expand_tiles<2>(a, groups * stripes, splits, stripe, stripes, s);
-  else expand_tiles<4>(a, groups * stripes, splits, stripe, stripes, s);
+  void (*fn)(AdapterArgs, int, int, int) = a.R <= 16   ? expand_tile_kernel<1>
+                                           : a.R <= 32 ? expand_tile_kernel<2>
+                                           : a.R <= 64 ? expand_tile_kernel<4>
+                                                       : expand_tile_kernel<8>;
+  fn<<<groups * stripes, 256, 0, s>>>(a, splits, stripe, stripes);
   return hipGetLastError();
 }
 
