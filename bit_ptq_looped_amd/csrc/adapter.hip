@@ -39,24 +39,59 @@ __device__ __forceinline__ void eight_bf16(const uint4& u, float (&v)[8]) {
 }
 
 // ---------------------------------------------------------------- few rows
+//
+// fp32 FMA of the vector units; A and B are read with 16 bytes a lane, eight
+// neighbours of K (ranks) each.
 
-constexpr int kRanks = 2;  // ranks a wave takes
+// Sums of V[0 .. n - 1] over the wave's lanes.  Two values change halves with one
+// swap of 32 lanes, then of 16: a lane goes on with a quarter of them; four
+// steps within 16 lanes finish.  sums() leaves value i of the V in the lanes
+// 16 q .. 16 q + 15 of v[i / 4], q = i % 4.
+template <int S>
+__device__ __forceinline__ float swap_add(float x, float y) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  u32x2 r;
+  if constexpr (S == 32) r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  else r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+template <int N>
+__device__ __forceinline__ void sums(float (&v)[N]) {
+  static_assert(N % 4 == 0, "four values share a lane's 16");
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    // lanes 0-15: value 4 i, 16-31: 4 i + 1, 32-47: 4 i + 2, 48-63: 4 i + 3
+    const float a = swap_add<32>(v[4 * i], v[4 * i + 2]), b = swap_add<32>(v[4 * i + 1], v[4 * i + 3]);
+    float x = swap_add<16>(a, b);
+    x = dpp_add<0xB1>(x);
+    x = dpp_add<0x4E>(x);
+    x = dpp_add<0x141>(x);
+    v[i] = dpp_add<0x140>(x);
+  }
+}
 
-// A wave forms kRanks of a row's z: products of 8 elements a lane and step, the
-// lanes added up by a butterfly.
+// A wave forms J ranks of a token's z, 512 elements of K a step.
+constexpr int J = 4;
 template <int BF>
 __global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m = blockIdx.x;
-  const int j0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * kRanks;
-  const int id = adapter_of(a, m);
+  const int j0 = (blockIdx.y * 4 + wave) * J;
+  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
   if (id < 0) return;
-  const int rank = rank_of(a, id);
+  const int rank = wave_rank_of(a, id);
   if (j0 >= rank) return;
   const uint16_t* A = a.A + ((int64_t)id * a.R + j0) * a.K;
-  float acc[kRanks] = {};
-#pragma unroll 4
+  float acc[J] = {};
+#pragma unroll 2
   for (int k = 8 * lane; k < a.K; k += 512) {
+    uint4 w[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) w[j] = *reinterpret_cast<const uint4*>(A + (int64_t)(j0 + j < rank ? j : 0) * a.K + k);
     float x[8];
     if constexpr (BF) {
       eight_bf16(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + m * a.ldx + k), x);
@@ -66,47 +101,36 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
       x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
     }
 #pragma unroll
-    for (int j = 0; j < kRanks; ++j) {
-      if (j0 + j >= rank) break;
-      float w[8];
-      eight_bf16(*reinterpret_cast<const uint4*>(A + (int64_t)j * a.K + k), w);
+    for (int j = 0; j < J; ++j) {
+      float u[8];
+      eight_bf16(w[j], u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[j] = __builtin_fmaf(x[i], w[i], acc[j]);
+      for (int i = 0; i < 8; ++i) acc[j] = __builtin_fmaf(x[i], u[i], acc[j]);
     }
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-#pragma unroll
-    for (int j = 0; j < kRanks; ++j) acc[j] += __shfl_xor(acc[j], o);
-  if (lane == 0) {
-    const float s = a.scales[id];
-#pragma unroll
-    for (int j = 0; j < kRanks; ++j)
-      if (j0 + j < rank) a.z[m * a.R + j0 + j] = s * acc[j];
-  }
+  sums(acc);
+  const int j = j0 + (lane >> 4);
+  if ((lane & 15) == 0 && j < rank) a.z[m * a.R + j] = a.scales[id] * acc[0];
 }
 
-// A wave adds to 64 elements of a row of y.  C = 2^k >= R / 8 lanes share an
-// element, eight ranks each (one 16-byte read of B), in C passes over the 64;
-// lane l keeps the element of pass l % C.
+// A wave adds to 64 outputs of a token of y.  C = 2^k >= R / 8 lanes share an output,
+// eight ranks each (one 16-byte read of B), in C passes over the 64; lane l keeps the
+// output of pass l % C.
 template <int C>
 __global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m = blockIdx.x;
-  const int n0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 64;
+  const int n0 = (blockIdx.y * 4 + wave) * 64;
   if (n0 >= a.N) return;
-  const int id = adapter_of(a, m);
+  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
   if (id < 0) return;
-  const int rank = rank_of(a, id);
+  const int rank = wave_rank_of(a, id);
   const int c = lane % C, per = 64 / C;
   const int n_mine = n0 + c * per + lane / C;
   float* y = a.y + m * a.ldy;
   float old = 0.0f;
   if (n_mine < a.N) old = y[n_mine];
   const int have = max(0, min(8, rank - 8 * c));  // ranks of this lane
-  float z[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = i < have ? a.z[m * a.R + 8 * c + i] : 0.0f;
   const uint16_t* B = a.B + ((int64_t)id * a.N) * a.R + 8 * c;
   uint4 b[C];
 #pragma unroll
@@ -114,6 +138,9 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
     const int n = n0 + p * per + lane / C;
     b[p] = n < a.N && have > 0 ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.R) : uint4{0u, 0u, 0u, 0u};
   }
+  float z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = i < have ? a.z[m * a.R + 8 * c + i] : 0.0f;
   float mine = 0.0f;
 #pragma unroll
   for (int p = 0; p < C; ++p) {
@@ -122,15 +149,17 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
     float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v = __builtin_fmaf(z[i], i < have ? w[i] : 0.0f, v);
-#pragma unroll
-    for (int o = 1; o < C; o <<= 1) v += __shfl_xor(v, o);
+    if constexpr (C > 1) v = dpp_add<0xB1>(v);
+    if constexpr (C > 2) v = dpp_add<0x4E>(v);
+    if constexpr (C > 4) v = dpp_add<0x141>(v);
+    if constexpr (C > 8) v = dpp_add<0x140>(v);
     if (c == p) mine = v;
   }
   if (n_mine < a.N) y[n_mine] = old + mine;
 }
 
 hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
-  const dim3 shrink(a.rows, (a.R + 4 * kRanks - 1) / (4 * kRanks));
+  const dim3 shrink(a.rows, (a.R + 4 * J - 1) / (4 * J));
   if (a.x_bf16) shrink_rows_kernel<1><<<shrink, 256, 0, s>>>(a);
   else shrink_rows_kernel<0><<<shrink, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
@@ -166,7 +195,7 @@ hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
 constexpr int kTile = 64;    // tokens of a shrink work-group, 16 a wave
 constexpr int kTokens = 128; // tokens of an expand work-group, 32 a wave
 constexpr int kFew = 6;
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 16;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -224,7 +253,8 @@ __device__ __forceinline__ void shrink_mm(const u32x4 (&w)[RT], const u32x4 (&x)
 
 // z partial sums (16x16x32 MFMA, ranks the first operand, tokens the second: a lane
 // ends with four ranks of a token): work-group (tile of 64 tokens, split of K), 16
-// tokens a wave.  K goes in chunks of 256 bytes a row of x.
+// tokens a wave.  K goes in chunks of 256 bytes a row of x, two of them on their way
+// while one is multiplied.
 // RT: rank tiles of 16 (R <= 16 RT).
 template <int BF, int RT>
 __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
@@ -255,10 +285,8 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
     if (my_id != ad) return;
     const float s = a.scales[ad];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * t + 4 * lq + e < rank) z[16 * t + 4 * lq + e] = s * acc[t][e];
+    for (int t = 0; t < RT; ++t)  // rows of z are whole multiples of eight: what lies past the rank is never read
+      if (16 * t + 4 * lq < rank) *reinterpret_cast<v4f*>(z + 16 * t + 4 * lq) = v4f{s * acc[t][0], s * acc[t][1], s * acc[t][2], s * acc[t][3]};
   };
   auto clear = [&]() {
 #pragma unroll
@@ -272,42 +300,53 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
     while (todo.left) {
       const int ad = todo.next(), rank = wave_rank_of(a, ad);
       const auto wr = resource(a.A + (int64_t)ad * a.R * a.K, (int64_t)rank * a.K * 2);  // rows from the rank on lie outside
-      u32x4 x[4], w[WN];
-      auto load = [&](int c) {
+      struct Chunk {
+        u32x4 x[4], w[WN];
+      };
+      // always the same number of loads, so that the wait for one chunk leaves the next ones under way
+      auto load = [&](Chunk& s, int c) {
         const int kx = c * KC + (int)(threadIdx.x & 15) * (16 / item);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          x[i] = load16(xr, xid[i] == ad && kx < a.K ? (uint32_t)((((int)(threadIdx.x >> 4) + 16 * i) * a.ldx + kx) * item) : kNone);
+          s.x[i] = load16(xr, xid[i] == ad && kx < a.K && c < c1 ? (uint32_t)((((int)(threadIdx.x >> 4) + 16 * i) * a.ldx + kx) * item) : kNone);
         const int kw = c * KC + (int)(threadIdx.x % WL) * 8;
 #pragma unroll
         for (int i = 0; i < WN; ++i) {
           const int j = (int)threadIdx.x / WL + i * (256 / WL);
-          w[i] = load16(wr, kw < a.K ? (uint32_t)((j * a.K + kw) * 2) : kNone);
+          s.w[i] = load16(wr, kw < a.K && c < c1 ? (uint32_t)((j * a.K + kw) * 2) : kNone);
         }
       };
-      clear();
-      load(c0);
-      for (int c = c0; c < c1; ++c) {
+      auto multiply = [&](Chunk& s, int next) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(sx + ((int)(threadIdx.x >> 4) + 16 * i) * XS + (threadIdx.x & 15) * 16) = x[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(sx + ((int)(threadIdx.x >> 4) + 16 * i) * XS + (threadIdx.x & 15) * 16) = s.x[i];
 #pragma unroll
         for (int i = 0; i < WN; ++i) {
           const int j = (int)threadIdx.x / WL + i * (256 / WL);
-          if (16 * RT * WL >= 256 || j < 16 * RT) *reinterpret_cast<u32x4*>(sw + j * WS + (threadIdx.x % WL) * 16) = w[i];
+          if (16 * RT * WL >= 256 || j < 16 * RT) *reinterpret_cast<u32x4*>(sw + j * WS + (threadIdx.x % WL) * 16) = s.w[i];
         }
         __syncthreads();
-        if (c + 1 < c1) load(c + 1);
+        load(s, next);
 #pragma unroll
-        for (int s = 0; s < KC / 32; ++s) {
+        for (int k = 0; k < KC / 32; ++k) {
           u32x4 xo[BF ? 1 : 2], wo[RT];
 #pragma unroll
           for (int p = 0; p < (BF ? 1 : 2); ++p)
-            xo[p] = *reinterpret_cast<const u32x4*>(sx + (16 * wave + li) * XS + (32 * s + 8 * lq) * item + 16 * p);
+            xo[p] = *reinterpret_cast<const u32x4*>(sx + (16 * wave + li) * XS + (32 * k + 8 * lq) * item + 16 * p);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) wo[t] = *reinterpret_cast<const u32x4*>(sw + (16 * t + li) * WS + (32 * s + 8 * lq) * 2);
+          for (int t = 0; t < RT; ++t) wo[t] = *reinterpret_cast<const u32x4*>(sw + (16 * t + li) * WS + (32 * k + 8 * lq) * 2);
           shrink_mm<BF, RT>(wo, xo, acc);
         }
+      };
+      clear();
+      Chunk s0, s1;
+      load(s0, c0);
+      load(s1, c0 + 1);
+      for (int c = c0;;) {
+        multiply(s0, c + 2);
+        if (++c >= c1) break;
+        multiply(s1, c + 2);
+        if (++c >= c1) break;
       }
       finish(ad, rank);
     }
@@ -368,12 +407,47 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
   }
 }
 
+// The splits' sums of z, added in their order, as three bf16 planes: [row][R / 8][3][8].
+// A thread takes eight ranks of a token; ranks that its adapter does not have are 0.
+// (Read by the next kernel itself, 16 splits of 1500 tokens cost it 9 us in each of 40
+// stripes of N, this launch 3.)
+__global__ __launch_bounds__(256) void join_kernel(AdapterArgs a, int splits) {
+  const int per = a.R / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = i / per;
+  if (m >= a.rows) return;
+  const int id = adapter_of(a, m);
+  if (id < 0) return;
+  const int j = (int)(i - m * per) * 8, rank = rank_of(a, id);
+  float v[8] = {};
+  if (j < rank) {
+    const float* at = a.z + m * a.R + j;
+#pragma unroll 4
+    for (int sp = 0; sp < splits; ++sp) {
+      const v4f* p = reinterpret_cast<const v4f*>(at + (int64_t)sp * a.rows * a.R);
+      const v4f u0 = p[0], u1 = p[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += u0[e];
+        v[4 + e] += u1[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = j + e < rank ? v[e] : 0.0f;
+  v4u planes[3];
+  planes8(v, planes);
+  v4u* to = reinterpret_cast<v4u*>(a.planes) + i * 3;
+#pragma unroll
+  for (int p = 0; p < 3; ++p) to[p] = planes[p];
+}
+
 // y += B z (32x32x16 MFMA, tokens the first operand, outputs the second: a lane ends
 // with 16 tokens of one output): work-group (128 tokens, stripe of N), 32 tokens a
-// wave.  NB outputs of B go through LDS at a time; the next ones and the y of the next
-// 32 are loaded while some are multiplied.  RS: steps of 16 ranks (R <= 16 RS).
+// wave.  NB outputs of B go through LDS at a time; the next ones, and their y, are
+// loaded while some are multiplied.  RS: steps of 16 ranks (R <= 16 RS).
 template <int RS>
-__global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int splits, int stripe, int stripes) {
+__global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(AdapterArgs a, int stripe, int stripes) {
   constexpr int NB = 64;                 // outputs of a block
   constexpr int BS = 32 * RS + 16;       // bytes of a row of B in LDS
   constexpr int BL = 2 * RS;             // lanes of a row
@@ -402,47 +476,43 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int spl
   }
   const int n_begin = (blockIdx.x - group * stripes) * stripe, n_end = min(a.N, n_begin + stripe);
   const auto yr = resource(a.y + m0 * a.ldy, 31 * a.ldy * 4 + (int64_t)a.N * 4);
+  // z of the wave's tokens
   u32x4 z[RS][3];
-  {
-    const int mine = id >= 0 ? rank_of(a, id) : 0;
+  auto load_z = [&]() {
+    const auto zr = resource(a.planes + m0 * a.R * 3, (int64_t)32 * a.R * 6);
 #pragma unroll
     for (int t = 0; t < RS; ++t) {
       const int j = 16 * t + 8 * lh;
-      float v[8] = {};
-      if (j < mine) {
-        for (int sp = 0; sp < splits; ++sp) {
-          const v4f* p = reinterpret_cast<const v4f*>(a.z + ((int64_t)sp * a.rows + m0 + li) * a.R + j);
-          const v4f u0 = p[0], u1 = p[1];
+      const uint32_t at = id >= 0 && j < a.R ? (uint32_t)((li * a.R + j) * 6) : kNone;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] += u0[e];
-            v[4 + e] += u1[e];
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = j + e < mine ? v[e] : 0.0f;
-      v4u planes[3];
-      planes8(v, planes);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) z[t][p] = planes[p];
+      for (int p = 0; p < 3; ++p) z[t][p] = load16(zr, at + 16 * p);
     }
-  }
-  // element e of a result is token 8 (e / 4) + 4 lh + e % 4, output li
-  uint32_t mine_of = 0;  // the adapter's tokens among this lane's
-  auto y_at = [&](int e, int n) {
-    const int tok = 8 * (e / 4) + 4 * lh + e % 4;
-    return (mine_of >> e & 1) && n < n_end ? (uint32_t)((tok * a.ldy + n) * 4) : kNone;
   };
-  auto set_mine = [&](int ad) {
+  // Element e of a result is token 8 (e / 4) + 4 lh + e % 4, output li: the lane's place
+  // and a row distance of the wave.  Tokens of other adapters are masked unless all 32
+  // are this one's.
+  uint32_t mine_of = 0;
+  bool whole = false;
+  const uint32_t lane_at = (uint32_t)(4 * lh * a.ldy * 4);
+  auto set_tokens = [&](uint64_t is) {
     mine_of = 0;
-    const uint64_t is = __ballot(ad >= 0 && id == ad);
+    whole = is == ~0ull;
 #pragma unroll
     for (int e = 0; e < 16; ++e) mine_of |= (uint32_t)(is >> (8 * (e / 4) + 4 * lh + e % 4) & 1) << e;
+    return is != 0;
   };
+  auto row_at = [&](int e) { return (int)((8 * (e / 4) + e % 4) * a.ldy * 4); };
   auto load_y = [&](v16f& old, int n) {
+    const uint32_t at = n + li < n_end ? lane_at + 4u * (n + li) : kNone;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, y_at(e, n + li), 0, 0));
+    for (int e = 0; e < 16; ++e)
+      old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, whole || (mine_of >> e & 1) ? at : kNone, row_at(e), 0));
+  };
+  auto store_y = [&](const v16f& old, const v16f& v, int n) {
+    const uint32_t at = n + li < n_end ? lane_at + 4u * (n + li) : kNone;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + v[e]), yr, whole || (mine_of >> e & 1) ? at : kNone, row_at(e), 0);
   };
   // ranks that an adapter does not have among a lane's eight of step t
   auto cut = [&](u32x4 v, int t, int rank) {
@@ -460,12 +530,11 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int spl
 #pragma unroll
       for (int t = 0; t < RS; ++t) acc = mm32(z[t][p], b[t], acc);
     mfma_settle_before_join();
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + acc[e]), yr, y_at(e, n + li), 0, 0);
+    store_y(old, acc, n);
   };
 
   if (few <= kFew) {
+    bool have_z = false;
     while (lower.left || upper.left) {
       int ad;
       if (lower.left) {
@@ -475,21 +544,17 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int spl
         ad = upper.next();
       }
       const int rank = wave_rank_of(a, ad);
-      set_mine(ad);
-      const bool any = __ballot(id == ad) != 0;
+      const bool any = set_tokens(__ballot(id == ad));
       const auto br = resource(a.B + (int64_t)ad * a.N * a.R, (int64_t)a.N * a.R * 2);  // outputs from N on lie outside
       u32x4 b[BN > 0 ? BN : 1];
       auto load_b = [&](int n0) {
 #pragma unroll
         for (int i = 0; i < (BN > 0 ? BN : 1); ++i) {
           const int n = (int)threadIdx.x / BL + i * (256 / BL), j = (int)(threadIdx.x % BL) * 8;
-          b[i] = load16(br, j < rank ? (uint32_t)(((n0 + n) * a.R + j) * 2) : kNone);
+          b[i] = load16(br, j < rank && n0 < n_end ? (uint32_t)(((n0 + n) * a.R + j) * 2) : kNone);
         }
       };
-      v16f old[2];
-      load_b(n_begin);
-      if (any) load_y(old[0], n_begin);
-      for (int n0 = n_begin; n0 < n_end; n0 += NB) {
+      auto stage_b = [&]() {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < (BN > 0 ? BN : 1); ++i) {
@@ -497,67 +562,108 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(AdapterArgs a, int spl
           if (BN > 0 || n < NB) *reinterpret_cast<u32x4*>(sb + n * BS + (threadIdx.x % BL) * 16) = b[i];
         }
         __syncthreads();
-        if (n0 + NB < n_end) load_b(n0 + NB);
-        if (!any) continue;
+      };
+      load_b(n_begin);
+      if (!any) {  // another wave's adapter: help with B
+        for (int n0 = n_begin; n0 < n_end; n0 += NB) {
+          stage_b();
+          load_b(n0 + NB);
+        }
+        continue;
+      }
+      v16f old[2];
+      load_y(old[0], n_begin);
+      load_y(old[1], n_begin + 32);
+      if (!have_z) load_z();
+      have_z = true;
+      for (int n0 = n_begin; n0 < n_end; n0 += NB) {
+        stage_b();
+        load_b(n0 + NB);
 #pragma unroll
-        for (int h = 0; h < NB / 32; ++h) {
-          load_y(old[(h + 1) & 1], n0 + 32 * (h + 1));
+        for (int h = 0; h < 2; ++h) {
           u32x4 bo[RS];
 #pragma unroll
-          for (int t = 0; t < RS; ++t) {
-            bo[t] = *reinterpret_cast<const u32x4*>(sb + (32 * h + li) * BS + (16 * t + 8 * lh) * 2);
-            if (rank & 7) bo[t] = cut(bo[t], t, rank);
+          for (int t = 0; t < RS; ++t) bo[t] = *reinterpret_cast<const u32x4*>(sb + (32 * h + li) * BS + (16 * t + 8 * lh) * 2);
+          if (rank & 7) {
+#pragma unroll
+            for (int t = 0; t < RS; ++t) bo[t] = cut(bo[t], t, rank);
           }
-          multiply(bo, old[h & 1], n0 + 32 * h);
+          multiply(bo, old[h], n0 + 32 * h);
+          load_y(old[h], n0 + NB + 32 * h);
         }
       }
     }
     return;
   }
 
-  // many adapters: a wave for itself
+  // many adapters: a wave for itself, 64 outputs at a time through its adapters; the
+  // result of each token is picked from its own's, y is read and written once
   Adapters own(id, 0xFFFFFFFFull);
-  int ad = own.next_or_none();
-  if (ad < 0) return;
-  auto load_own = [&](u32x4 (&b)[RS], int of, int rank, int n) {
+  if (own.left == 0) return;
+  load_z();
+  set_tokens(__ballot(id >= 0));
+  struct Part {
+    u32x4 b[2][RS];
+  };
+  // always the same number of loads, so that the wait for one part leaves the next one's under way
+  auto load_part = [&](Part& s, int of, int rank, int n) {
     const auto br = resource(a.B + (int64_t)max(of, 0) * a.N * a.R, of < 0 ? 0 : (int64_t)a.N * a.R * 2);
 #pragma unroll
-    for (int t = 0; t < RS; ++t) {
-      const int j = 16 * t + 8 * lh;
-      b[t] = load16(br, j < rank ? (uint32_t)(((n + li) * a.R + j) * 2) : kNone);
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < RS; ++t) {
+        const int j = 16 * t + 8 * lh;
+        s.b[h][t] = load16(br, j < rank ? (uint32_t)(((n + 32 * h + li) * a.R + j) * 2) : kNone);
+      }
   };
-  while (ad >= 0) {
-    const int rank = wave_rank_of(a, ad);
-    set_mine(ad);
-    u32x4 b0[RS], b1[RS];
-    v16f y0, y1;
-    load_own(b0, ad, rank, n_begin);
-    load_y(y0, n_begin);
-    for (int n = n_begin; n < n_end; n += 64) {
-      load_own(b1, ad, rank, n + 32);
-      load_y(y1, n + 32);
-      if (rank & 7) {
+  for (int n = n_begin; n < n_end; n += NB) {
+    v16f old[2], got[2] = {};
+    load_y(old[0], n);
+    load_y(old[1], n + 32);
+    Adapters left = own;
+    auto pick = [&](Part& s, int of, int rank) {
+      const uint64_t is = __ballot(id == of);
 #pragma unroll
-        for (int t = 0; t < RS; ++t) b0[t] = cut(b0[t], t, rank);
-      }
-      multiply(b0, y0, n);
-      if (n + 32 >= n_end) break;
-      load_own(b0, ad, rank, n + 64);
-      load_y(y0, n + 64);
-      if (rank & 7) {
+      for (int h = 0; h < 2; ++h) {
+        if (rank & 7) {
 #pragma unroll
-        for (int t = 0; t < RS; ++t) b1[t] = cut(b1[t], t, rank);
+          for (int t = 0; t < RS; ++t) s.b[h][t] = cut(s.b[h][t], t, rank);
+        }
+        v16f acc = {};
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int t = 0; t < RS; ++t) acc = mm32(z[t][p], s.b[h][t], acc);
+        mfma_settle_before_join();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) got[h][e] = is >> (8 * (e / 4) + 4 * lh + e % 4) & 1 ? acc[e] : got[h][e];
       }
-      multiply(b1, y1, n + 32);
+    };
+    int ad = left.next(), rank = wave_rank_of(a, ad);
+    Part p0, p1;
+    load_part(p0, ad, rank, n);
+    for (;;) {
+      int of = ad, of_rank = rank;
+      ad = left.next_or_none();
+      if (ad >= 0) rank = wave_rank_of(a, ad);
+      load_part(p1, ad, rank, n);
+      pick(p0, of, of_rank);
+      if (ad < 0) break;
+      of = ad, of_rank = rank;
+      ad = left.next_or_none();
+      if (ad >= 0) rank = wave_rank_of(a, ad);
+      load_part(p0, ad, rank, n);
+      pick(p1, of, of_rank);
+      if (ad < 0) break;
     }
-    ad = own.next_or_none();
+    store_y(old[0], got[0], n);
+    store_y(old[1], got[1], n + 32);
   }
 }
 
 int splits_for(int64_t rows, int K) {
   const int64_t tiles = (rows + kTile - 1) / kTile;
-  const int64_t want = 768 / tiles, most = (K + 511) / 512;
+  const int64_t want = 512 / tiles, most = (K + 255) / 256;
   const int64_t n = want < most ? want : most;
   return (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
@@ -577,28 +683,35 @@ hipError_t launch_tiles(const AdapterArgs& a, hipStream_t s) {
   else shrink_tiles<8>(a, shrink, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  join_kernel<<<(unsigned)(((int64_t)a.rows * (a.R / 8) + 255) / 256), 256, 0, s>>>(a, splits);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const int groups = (a.rows + kTokens - 1) / kTokens, blocks = (a.N + 63) / 64;
-  int stripes = (1536 + groups - 1) / groups;
+  int stripes = ((a.R <= 64 ? 1536 : 1024) + groups - 1) / groups;  // with 3 and 2 work-groups a CU
   if (stripes > blocks) stripes = blocks;
   const int stripe = (blocks + stripes - 1) / stripes * 64;
   stripes = (a.N + stripe - 1) / stripe;
-  void (*fn)(AdapterArgs, int, int, int) = a.R <= 16   ? expand_tile_kernel<1>
+  void (*fn)(AdapterArgs, int, int) = a.R <= 16   ? expand_tile_kernel<1>
                                            : a.R <= 32 ? expand_tile_kernel<2>
                                            : a.R <= 64 ? expand_tile_kernel<4>
                                                        : expand_tile_kernel<8>;
-  fn<<<groups * stripes, 256, 0, s>>>(a, splits, stripe, stripes);
+  fn<<<groups * stripes, 256, 0, s>>>(a, stripe, stripes);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// z of each split of K (at most what splits_for gives for any K)
-size_t adapter_workspace_bytes(int64_t rows, int max_rank) {
+// z of each split of K (at most what splits_for gives for any K), and its planes
+static size_t sums_bytes(int64_t rows, int max_rank) {
   return (size_t)(splits_for(rows > 0 ? rows : 1, 1 << 30) * rows * max_rank * 4 + 255) / 256 * 256;
 }
+size_t adapter_workspace_bytes(int64_t rows, int max_rank) {
+  return sums_bytes(rows, max_rank) + (size_t)(rows * max_rank * 6 + 255) / 256 * 256;
+}
 
-hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s) {
-  return a.rows <= 64 ? launch_rows(a, s) : launch_tiles(a, s);
+hipError_t launch_adapter(AdapterArgs a, hipStream_t s) {
+  a.planes = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(a.z) + sums_bytes(a.rows, a.R));
+  return a.rows <= 256 ? launch_rows(a, s) : launch_tiles(a, s);
 }
 
 }  // namespace loopq

@@ -70,9 +70,10 @@ struct AdapterArgs {
   int adapters, R;
   float* y;
   int64_t ldy;
-  float* z;              // [rows][R]
+  float* z;              // workspace: [splits][rows][R]
+  uint16_t* planes;      // behind it: bf16 [rows][R / 8][3][8] (set by the launcher)
 };
 size_t adapter_workspace_bytes(int64_t rows, int max_rank);
-hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
+hipError_t launch_adapter(AdapterArgs a, hipStream_t s);
 
 }  // namespace loopq
