@@ -13,7 +13,7 @@ from typing import NamedTuple
 
 from . import kv, loopq
 from .kv import KVTable, _ints, _pool, _ref, _rows3, _table
-from .loopq import _check, _dtype_code, _ptr, _stream
+from .loopq import _check, _dtype_code, _stream
 
 LOOPQ_ROPE_HALF, LOOPQ_ROPE_PAIRS = 0, 1
 LOOPQ_ROPE_PLAIN, LOOPQ_ROPE_LINEAR, LOOPQ_ROPE_BASE, LOOPQ_ROPE_PARTS = 0, 1, 2, 3
@@ -61,29 +61,43 @@ def load():
     return _lib
 
 
+_torch = None
+_codes = None  # dtype code of each type of activations
+
+
+def _types():
+    global _torch, _codes
+    if _torch is None:
+        torch = loopq._torch_mod()
+        _codes = {torch.float32: loopq.LOOPQ_F32, torch.bfloat16: loopq.LOOPQ_BF16}
+        _torch = torch
+    return _torch
+
+
 def _on(t, stream):
     """The stream of a call whose first tensor is t: the current device's, where t has to live."""
-    if t.device.index != loopq._torch_mod().cuda.current_device():
+    if t.get_device() != _torch._C._cuda_getDevice():
         raise ValueError("the tensors' device must be the current one")
     return _stream(stream)
 
 
 def _rows2(t, what: str, rows: int, width: int):
     """Pointer, row distance and dtype code of [rows][width] with dense rows."""
-    if tuple(t.shape) != (rows, width) or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected [{rows}][{width}] with dense rows")
-    return _ptr(t), (t.stride(0) if rows > 1 else width), _dtype_code(t)
+    code = _codes.get(t.dtype)
+    if t.shape != (rows, width) or (width > 1 and t.stride(1) != 1) or code is None or not t.is_cuda:
+        raise ValueError(f"{what}: expected [{rows}][{width}] of float32 or bfloat16 with dense rows on the GPU")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else width), code
 
 
 def _dense(t, what: str, dtype, n: int):
-    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: a contiguous {dtype} tensor of at least {n} values")
-    return _ptr(t)
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n or not t.is_cuda:
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of at least {n} values on the GPU")
+    return t.data_ptr()
 
 
 def _rope(r: Rope) -> _Rope:
     f = r.inv_freq
-    return _Rope(_dense(f, "inv_freq", loopq._torch_mod().float64, 1), 2 * f.numel(), r.layout, r.magnitude)
+    return _Rope(_dense(f, "inv_freq", _types().float64, 1), 2 * f.numel(), r.layout, r.magnitude)
 
 
 # ----------------------------------------------------------------- host-only calls
@@ -108,7 +122,7 @@ def loopq_adapter_workspace_bytes(rows: int, max_rank: int) -> int:
 def loopq_rms_norm(x, weight, eps: float, y=None, residual=None, sum_out=None, codes=None, steps=None,
                    clip: float = 1.0, bits_a: int = 8, per_token: bool = False, stream=None):
     """x [rows][K] (+ residual) through the RMS norm into y and / or Eq.(4) codes and steps."""
-    torch = loopq._torch_mod()
+    torch = _types()
     rows, K = x.shape
     xp = _rows2(x, "x", rows, K)
     rp = _rows2(residual, "residual", rows, K) if residual is not None else (None, 0, 0)
@@ -129,6 +143,7 @@ def loopq_rms_norm(x, weight, eps: float, y=None, residual=None, sum_out=None, c
 
 def loopq_rope(x, positions, rope: Rope, out, stream=None):
     """x, out [tokens][heads][head_dim], positions int32 [tokens]; out may be x itself."""
+    _types()
     tokens, heads, dim = x.shape
     xp, ldx = _rows3(x, None, dim, "x")
     op, ldo = _rows3(out, heads, dim, "out")
@@ -141,6 +156,7 @@ def loopq_rope(x, positions, rope: Rope, out, stream=None):
 def loopq_kv_write_rope(pool, slab: int, table: KVTable, cu, rope: Rope, k, v, q=None, q_out=None, stream=None):
     """k turned and v into a slab as the last tokens of each row, q turned into q_out
     (bfloat16 or float32; q itself if it has that type)."""
+    _types()
     p = _pool(pool)
     kp, ldk = _rows3(k, p.heads, p.head_dim, "k")
     vp, ldv = _rows3(v, p.heads, p.head_dim, "v")
@@ -163,7 +179,7 @@ def loopq_adapter_apply(x, ids, A, B, scales, y, workspace, ranks=None, stream=N
     """y [rows][N] float32 += scales[a] B[a] (A[a] x) for the adapter a = ids[row] of each row.
 
     x [rows][K], A bfloat16 [adapters][max_rank][K], B bfloat16 [adapters][N][max_rank]."""
-    torch = loopq._torch_mod()
+    torch = _types()
     rows, K = x.shape
     n, rank, width = A.shape
     if width != K or B.shape[0] != n or B.shape[2] != rank:

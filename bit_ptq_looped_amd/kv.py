@@ -89,7 +89,7 @@ def _types():
 
 
 def _ints(t, what: str, n: int = 0) -> int:
-    if t.dtype is not _types().int32 or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not (_torch or _types()).int32 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} values")
     return _ptr(t)
 
