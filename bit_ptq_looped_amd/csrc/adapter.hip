@@ -353,17 +353,22 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
     return;
   }
 
-  // many adapters: a wave for itself, two sets of registers, KS MFMA steps each
+  // many adapters: a wave for itself, two register sets of KS MFMA steps each
   constexpr int KS = RT == 1 ? 4 : RT <= 4 ? 2 : 1;
   struct Step {
     u32x4 x[KS][BF ? 1 : 2];
     u32x4 w[KS][RT];
+    int ad, rank, k0;
   };
   Adapters own(my_id, 0xFFFFull);
   const uint32_t xat = (uint32_t)((16 * wave + li) * a.ldx * item);
-  const int k_end = min(a.K, c1 * KC);
-  // always the same number of loads, so that the wait for one step leaves the next one's under way
-  auto load = [&](Step& s, int ad, int rank, int k0) {
+  const int k_begin = c0 * KC, k_end = min(a.K, c1 * KC);
+  if (own.left == 0 || k_begin >= k_end) return;
+  int ad = own.next(), rank = wave_rank_of(a, ad), k0 = k_begin;
+  // the step at hand, and on to the next; always the same number of loads, so that the
+  // wait for one step leaves the next one's under way
+  auto load = [&](Step& s) {
+    s.ad = ad, s.rank = rank, s.k0 = k0;
     const auto wr = resource(a.A + (int64_t)max(ad, 0) * a.R * a.K, ad < 0 ? 0 : (int64_t)rank * a.K * 2);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
@@ -375,35 +380,26 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) s.w[i][t] = load16(wr, in ? (uint32_t)(((16 * t + li) * a.K + k) * 2) : kNone);
     }
-  };
-  int ad = own.next_or_none(), k0 = c0 * KC;
-  if (ad < 0 || c0 >= c1) return;
-  int rank = wave_rank_of(a, ad);
-  auto advance = [&]() {
     if ((k0 += 32 * KS) < k_end) return;
-    ad = own.next_or_none();
+    k0 = k_begin;
+    ad = ad < 0 ? -1 : own.next_or_none();
     if (ad >= 0) rank = wave_rank_of(a, ad);
-    k0 = c0 * KC;
   };
-  auto multiply = [&](const Step& s, int of, int of_rank, int at) {
-    if (at == c0 * KC) clear();
+  auto multiply = [&](const Step& s) {
+    if (s.k0 == k_begin) clear();
 #pragma unroll
     for (int i = 0; i < KS; ++i) shrink_mm<BF, RT>(s.w[i], s.x[i], acc);
-    if (at + 32 * KS >= k_end) finish(of, of_rank);
+    if (s.k0 + 32 * KS >= k_end) finish(s.ad, s.rank);
   };
   Step s0, s1;
-  load(s0, ad, rank, k0);
+  load(s0);
   for (;;) {
-    int at = k0, of = ad, of_rank = rank;
-    advance();
-    load(s1, ad, rank, k0);
-    multiply(s0, of, of_rank, at);
-    if (ad < 0) break;
-    at = k0, of = ad, of_rank = rank;
-    advance();
-    load(s0, ad, rank, k0);
-    multiply(s1, of, of_rank, at);
-    if (ad < 0) break;
+    load(s1);
+    multiply(s0);
+    if (s1.ad < 0) return;
+    load(s0);
+    multiply(s1);
+    if (s0.ad < 0) return;
   }
 }
 
@@ -491,14 +487,14 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
   // Element e of a result is token 8 (e / 4) + 4 lh + e % 4, output li: the lane's place
   // and a row distance of the wave.  Tokens of other adapters are masked unless all 32
   // are this one's.
+  // (lane_tokens: bit 8 (e / 4) + e % 4 is the lane's token e)
+  auto lane_tokens = [&](uint64_t is) { return lh ? (uint32_t)(is >> 4) : (uint32_t)is; };
   uint32_t mine_of = 0;
   bool whole = false;
   const uint32_t lane_at = (uint32_t)(4 * lh * a.ldy * 4);
   auto set_tokens = [&](uint64_t is) {
-    mine_of = 0;
+    mine_of = lane_tokens(is);
     whole = is == ~0ull;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) mine_of |= (uint32_t)(is >> (8 * (e / 4) + 4 * lh + e % 4) & 1) << e;
     return is != 0;
   };
   auto row_at = [&](int e) { return (int)((8 * (e / 4) + e % 4) * a.ldy * 4); };
@@ -506,13 +502,13 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
     const uint32_t at = n + li < n_end ? lane_at + 4u * (n + li) : kNone;
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, whole || (mine_of >> e & 1) ? at : kNone, row_at(e), 0));
+      old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, whole || (mine_of & (1u << (8 * (e / 4) + e % 4))) ? at : kNone, row_at(e), 0));
   };
   auto store_y = [&](const v16f& old, const v16f& v, int n) {
     const uint32_t at = n + li < n_end ? lane_at + 4u * (n + li) : kNone;
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + v[e]), yr, whole || (mine_of >> e & 1) ? at : kNone, row_at(e), 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + v[e]), yr, whole || (mine_of & (1u << (8 * (e / 4) + e % 4))) ? at : kNone, row_at(e), 0);
   };
   // ranks that an adapter does not have among a lane's eight of step t
   auto cut = [&](u32x4 v, int t, int rank) {
@@ -604,30 +600,34 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
   set_tokens(__ballot(id >= 0));
   struct Part {
     u32x4 b[2][RS];
-  };
-  // always the same number of loads, so that the wait for one part leaves the next one's under way
-  auto load_part = [&](Part& s, int of, int rank, int n) {
-    const auto br = resource(a.B + (int64_t)max(of, 0) * a.N * a.R, of < 0 ? 0 : (int64_t)a.N * a.R * 2);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int t = 0; t < RS; ++t) {
-        const int j = 16 * t + 8 * lh;
-        s.b[h][t] = load16(br, j < rank ? (uint32_t)(((n + 32 * h + li) * a.R + j) * 2) : kNone);
-      }
+    int ad, rank;
   };
   for (int n = n_begin; n < n_end; n += NB) {
     v16f old[2], got[2] = {};
     load_y(old[0], n);
     load_y(old[1], n + 32);
     Adapters left = own;
-    auto pick = [&](Part& s, int of, int rank) {
-      const uint64_t is = __ballot(id == of);
+    // the next adapter's part of B; always the same number of loads, so that the wait for
+    // one part leaves the next one's under way
+    auto load_part = [&](Part& s) {
+      s.ad = left.next_or_none();
+      s.rank = s.ad >= 0 ? wave_rank_of(a, s.ad) : 0;
+      const auto br = resource(a.B + (int64_t)max(s.ad, 0) * a.N * a.R, (int64_t)a.N * a.R * 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < RS; ++t) {
+          const int j = 16 * t + 8 * lh;
+          s.b[h][t] = load16(br, j < s.rank ? (uint32_t)(((n + 32 * h + li) * a.R + j) * 2) : kNone);
+        }
+    };
+    auto pick = [&](Part& s) {
+      const uint32_t is = lane_tokens(__ballot(id == s.ad));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (rank & 7) {
+        if (s.rank & 7) {
 #pragma unroll
-          for (int t = 0; t < RS; ++t) s.b[h][t] = cut(s.b[h][t], t, rank);
+          for (int t = 0; t < RS; ++t) s.b[h][t] = cut(s.b[h][t], t, s.rank);
         }
         v16f acc = {};
 #pragma unroll
@@ -636,25 +636,18 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
           for (int t = 0; t < RS; ++t) acc = mm32(z[t][p], s.b[h][t], acc);
         mfma_settle_before_join();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) got[h][e] = is >> (8 * (e / 4) + 4 * lh + e % 4) & 1 ? acc[e] : got[h][e];
+        for (int e = 0; e < 16; ++e) got[h][e] = is & (1u << (8 * (e / 4) + e % 4)) ? acc[e] : got[h][e];
       }
     };
-    int ad = left.next(), rank = wave_rank_of(a, ad);
     Part p0, p1;
-    load_part(p0, ad, rank, n);
+    load_part(p0);
     for (;;) {
-      int of = ad, of_rank = rank;
-      ad = left.next_or_none();
-      if (ad >= 0) rank = wave_rank_of(a, ad);
-      load_part(p1, ad, rank, n);
-      pick(p0, of, of_rank);
-      if (ad < 0) break;
-      of = ad, of_rank = rank;
-      ad = left.next_or_none();
-      if (ad >= 0) rank = wave_rank_of(a, ad);
-      load_part(p0, ad, rank, n);
-      pick(p1, of, of_rank);
-      if (ad < 0) break;
+      load_part(p1);
+      pick(p0);
+      if (p1.ad < 0) break;
+      load_part(p0);
+      pick(p1);
+      if (p0.ad < 0) break;
     }
     store_y(old[0], got[0], n);
     store_y(old[1], got[1], n + 32);
@@ -663,7 +656,7 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
 
 int splits_for(int64_t rows, int K) {
   const int64_t tiles = (rows + kTile - 1) / kTile;
-  const int64_t want = 512 / tiles, most = (K + 255) / 256;
+  const int64_t want = 512 / tiles, most = (K + 127) / 128;
   const int64_t n = want < most ? want : most;
   return (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
