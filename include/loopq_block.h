@@ -126,12 +126,13 @@ int32_t loopq_kv_write_rope(const loopq_kv_pool* pool_host, int32_t slab, const 
  * least); scales fp32 [adapters]; ranks int32 [adapters] or NULL: adapter a uses
  * the first ranks[a] (within 0 .. max_rank) rows of A_a and columns of B_a, the rest
  * is not used, whatever it holds.  ids, scales, ranks: device, 4-byte aligned.
- * Products of x and A and of A x and B are formed from all bits of their factors,
- * sums are fp32 in an order that depends on the sizes only (a row's result does
- * not depend on other rows' ids).  An infinity or NaN in a row or an adapter
- * reaches no row but its own.
+ * Products of x and A and of A x and B are formed from all bits of their factors
+ * (of 2^-100 and more in magnitude), sums are fp32 in an order that depends on
+ * the sizes only: a row's result does not depend on other rows' ids.  An infinity
+ * or NaN in a row or an adapter reaches no row but its own.
  * max_rank a multiple of 8 up to 128; K % 8 == 0, K <= 65536; N <= 2^20;
- * adapters <= 2^16; rows <= 2^20; ldx, ldy < 2^24.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank). */
+ * adapters <= 2^16; rows <= 2^20; ldx, ldy < 2^24.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank);
+ * two calls that share one must not overlap. */
 int32_t loopq_adapter_workspace_bytes(int32_t rows, int32_t max_rank, size_t* bytes_host);
 int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t rows, int32_t K, int32_t N,
                             const int32_t* ids, const void* A, const void* B, const float* scales,

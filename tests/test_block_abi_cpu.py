@@ -202,7 +202,7 @@ def adapter(lib, **kw):
     (dict(y=None), INVALID), (dict(ldx=56), INVALID), (dict(ldy=47), INVALID), (dict(x=FAKE + 8), ALIGNMENT), (dict(ldx=66), ALIGNMENT),
     (dict(ids=FAKE + MB + 2), ALIGNMENT), (dict(A=FAKE + 2 * MB + 8), ALIGNMENT), (dict(B=FAKE + 3 * MB + 8), ALIGNMENT),
     (dict(scales=FAKE + 4 * MB + 1), ALIGNMENT), (dict(ranks=FAKE + 5 * MB + 2), ALIGNMENT), (dict(y=FAKE + 6 * MB + 2), ALIGNMENT),
-    (dict(y=FAKE), INVALID), (dict(y=FAKE + 256), INVALID), (dict(ws=None), WORKSPACE), (dict(size=0), WORKSPACE), (dict(ws=FAKE + 7 * MB + 64), ALIGNMENT)])
+    (dict(ldx=1 << 24), UNSUPPORTED), (dict(ldy=1 << 24), UNSUPPORTED), (dict(y=FAKE), INVALID), (dict(y=FAKE + 256), INVALID), (dict(ws=None), WORKSPACE), (dict(size=0), WORKSPACE), (dict(ws=FAKE + 7 * MB + 64), ALIGNMENT)])
 def test_adapter_arguments(lib, kw, want):
     assert adapter(lib, **kw) == want
 

@@ -64,7 +64,8 @@ def whole(rng, rows, K, N, n, R):
 SIZES = [  # rows, K, N, adapters, max_rank
     (1, 8, 1, 1, 8), (1, 2048, 6144, 4, 16), (3, 520, 70, 2, 24), (16, 1024, 333, 5, 8), (17, 2560, 260, 3, 40),
     (48, 2560, 512, 32, 16), (64, 136, 129, 7, 128), (65, 384, 192, 4, 64), (100, 6912, 256, 8, 32), (129, 640, 68, 2, 72),
-    (500, 2048, 1000, 6, 16), (700, 5632, 130, 3, 48), (1031, 264, 260, 40, 8), (2100, 512, 515, 5, 128), (5000, 96, 64, 3, 16)]
+    (500, 2048, 1000, 6, 16), (700, 5632, 130, 3, 48), (1031, 264, 260, 40, 8), (2100, 512, 515, 5, 128), (5000, 96, 64, 3, 16),
+    (257, 8, 1, 3, 8), (300, 136, 77, 2, 24), (400, 520, 200, 20, 64), (320, 1032, 130, 9, 128), (600, 2048, 65, 70, 32), (1200, 304, 260, 30, 48)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -158,7 +159,8 @@ def test_strides_and_rows_without_an_adapter(lq, rows, K, N, n, R):
     assert (got == 3.5).all()
 
 
-@pytest.mark.parametrize("rows,K,N,n,R", [(9, 1024, 300, 4, 16), (260, 1024, 300, 4, 64), (1300, 640, 100, 8, 16)])
+@pytest.mark.parametrize("rows,K,N,n,R", [(9, 1024, 300, 4, 16), (260, 1024, 300, 4, 64), (1300, 640, 100, 8, 16), (700, 2048, 300, 12, 64),
+                                             (300, 640, 130, 9, 128), (1000, 1024, 68, 40, 24)])
 def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
     rng = np.random.default_rng(rows)
     x, A, B = dev(rng.standard_normal((rows, K))), dev(rng.standard_normal((n, R, K)), BF16), dev(rng.standard_normal((n, N, R)), BF16)
@@ -173,6 +175,22 @@ def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
         apply(x, np.full(rows, a), A, B, s, one)
         mine = torch.from_numpy(ids == a).cuda()
         assert torch.equal(one[mine], mixed[mine])
+
+
+@pytest.mark.parametrize("rows", [40, 300])
+def test_rows_far_apart(lq, rows):
+    """Row distances at the limit: a tile spans almost 2^31 bytes, the matrix much more."""
+    rng = np.random.default_rng(rows)
+    K, N, n, R, ld = 264, 68, 3, 16, (1 << 24) - 8
+    x, A, B, s, y = whole(rng, rows, K, N, n, R)
+    ids = np.sort(rng.integers(-1, n, rows))
+    want, _ = reference(x, ids, A, B, s, None, y)
+    xw = torch.empty((rows - 1) * ld + K, dtype=BF16, device="cuda").as_strided((rows, K), (ld, 1))
+    yw = torch.empty((rows - 1) * ld + N, device="cuda").as_strided((rows, N), (ld, 1))
+    xw.copy_(dev(x, BF16))
+    yw.copy_(dev(y))
+    apply(xw, ids, dev(A, BF16), dev(B, BF16), dev(s, F32), yw)
+    assert torch.equal(yw.double().cpu(), torch.from_numpy(want))
 
 
 def test_no_rows_and_no_adapters(lq):

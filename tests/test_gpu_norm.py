@@ -197,6 +197,26 @@ def test_many_short_rows(lq):
     check(x, None, None, out)
 
 
+def test_offsets_past_32_bits(lq):
+    rows, K = 66_000, 32768
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    y, codes = torch.empty_like(x), torch.empty((rows, K), dtype=torch.int8, device="cuda")
+    steps = torch.empty((rows, K // 32), device="cuda")
+    x[-3:] = make(3, K, torch.bfloat16, 25)
+    block.loopq_rms_norm(x, None, float(EPS), y=y, codes=codes, steps=steps, bits_a=8)
+    check(x[-3:], None, None, dict(y=y[-3:], sum_out=None, codes=codes[-3:], steps=steps[-3:]), bits=8)
+    assert not y[:-3].any() and not codes[:-3].any()
+
+
+def test_calls_are_recorded(lq):
+    x = make(3, 64, torch.float32, 26)
+    lq.loopq_timing_reset()
+    lq.loopq_timing_enable(True)
+    run(x, None, None, torch.float32)
+    lq.loopq_timing_enable(False)
+    assert lq.loopq_timing_read()[lq.LOOPQ_KERNEL_NORM][1] == 1
+
+
 def test_on_a_stream_and_in_a_graph(lq):
     x, res, w = make(37, 2560, torch.float32, 22), make(37, 2560, torch.bfloat16, 23), make(1, 2560, torch.float32, 24)[0]
     want = run(x, res, w, torch.bfloat16, codes=True, bits_a=4)

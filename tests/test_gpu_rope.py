@@ -107,6 +107,18 @@ def test_the_negative_turn_is_the_transposed_one(lq, dim, rot, layout):
         assert abs(slope - float(grad[t, h, e])) <= 4 * 5e-7 * float(g.abs().max())
 
 
+@pytest.mark.parametrize("rot", [128, 100])
+def test_offsets_past_32_bits(lq, rot):
+    tokens, heads = 2100, 8192
+    x, f = torch.zeros((tokens, heads, 128), dtype=BF16, device="cuda"), freqs(rot)
+    x[-1] = make((heads, 128), BF16, rot)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    want, err = turn(x[-1:].double().cpu().numpy(), [tokens - 1], f, HALF, 1.0)
+    block.loopq_rope(x, pos, spec(f), x)
+    close(x[-1:], want, err)
+    assert not x[:-1].any()
+
+
 def test_columns_of_wider_rows(lq):
     wide = make((50, 3 * 256 + 64), BF16, 5)
     before = wide.clone()
