@@ -35,7 +35,8 @@ int32_t check_rope(const loopq_rope_spec* r, int head_dim) {
   return aligned(r->inv_freq, 8) ? LOOPQ_OK : LOOPQ_ERR_ALIGNMENT;
 }
 
-// tokens of a rotary call: a launch has fewer than 2^32 work-items, 64 a token
+// tokens of a rotary call: a launch has fewer than 2^32 work-items, 64 a token (and a
+// token is shared by several waves only where there are fewer than 4096)
 constexpr int32_t kRopeMaxTokens = (1 << 26) - 4;
 
 RopeArgs rope_args(const loopq_rope_spec* r, int32_t dtype, int32_t tokens, int32_t head_dim) {
@@ -127,7 +128,7 @@ int32_t loopq_rms_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* 
 
 int32_t loopq_rope_frequencies(int32_t scaling, int32_t rot_dim, double base, double factor, double length, double low,
                                double high, double* inv_freq) {
-  if (!inv_freq || !(base > 1.0) || !isfinite(base)) return LOOPQ_ERR_INVALID_ARG;
+  if (!inv_freq || !(base > 1.0)) return LOOPQ_ERR_INVALID_ARG;
   if (scaling < LOOPQ_ROPE_PLAIN || scaling > LOOPQ_ROPE_PARTS) return LOOPQ_ERR_INVALID_ARG;
   if (rot_dim < 2 || rot_dim > 128 || rot_dim % 2 || (scaling == LOOPQ_ROPE_BASE && rot_dim < 4)) return LOOPQ_ERR_UNSUPPORTED;
   if (scaling != LOOPQ_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return LOOPQ_ERR_INVALID_ARG;
@@ -135,6 +136,7 @@ int32_t loopq_rope_frequencies(int32_t scaling, int32_t rot_dim, double base, do
       (!(length > 0.0) || !isfinite(length) || !(low >= 0.0) || !(high > low) || !isfinite(high)))
     return LOOPQ_ERR_INVALID_ARG;
   if (scaling == LOOPQ_ROPE_BASE) base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+  if (!isfinite(base)) return LOOPQ_ERR_INVALID_ARG;
   for (int i = 0; i < rot_dim / 2; ++i) {
     double f = pow(base, -2.0 * i / rot_dim);
     if (scaling == LOOPQ_ROPE_LINEAR) f /= factor;
@@ -242,8 +244,7 @@ int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t r
   int32_t st = check_rows(x, ldx, K, rows, dtype);
   if (st != LOOPQ_OK) return st;
   if (rows > 1 && ldy < N) return LOOPQ_ERR_INVALID_ARG;
-  // a tile of 32 rows lies within 2^31 bytes
-  if (rows > 1 && (ldx >= kAdapterMaxLd || ldy >= kAdapterMaxLd)) return LOOPQ_ERR_UNSUPPORTED;
+  if (rows > 1 && (ldx >= kAdapterMaxLdx / item_bytes(dtype) || ldy >= kAdapterMaxLdy / 4)) return LOOPQ_ERR_UNSUPPORTED;
   if (!aligned(ids, 4) || !aligned(A, 16) || !aligned(B, 16) || !aligned(scales, 4) || !aligned(ranks, 4) || !aligned(y, 4))
     return LOOPQ_ERR_ALIGNMENT;
   AdapterArgs a;

@@ -57,7 +57,8 @@ hipError_t launch_rope(RopeArgs a, hipStream_t s);
 
 constexpr int kAdapterMaxRank = 128;
 constexpr int kAdapterMaxRows = 1 << 20;
-constexpr int64_t kAdapterMaxLd = 1 << 24;  // 32 rows of fp32 stay below 2^31 bytes
+// bytes between rows: 64 rows of x, or 32 of y, lie within 2^31 bytes
+constexpr int64_t kAdapterMaxLdx = 1 << 25, kAdapterMaxLdy = 1 << 26;
 struct AdapterArgs {
   const void* x;
   int64_t ldx;           // elements

@@ -268,8 +268,6 @@ hipError_t launch_rope(RopeArgs a, hipStream_t s) {
   int split = want < passes ? want : passes;
   a.per = (passes + split - 1) / split * step;
   a.split = (a.heads + a.per - 1) / a.per;
-  // a launch has fewer than 2^32 work-items
-  if (((int64_t)a.tokens * a.split + 3) / 4 * 256 >= ((int64_t)1 << 32)) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(((int64_t)a.tokens * a.split + 3) / 4);
   void (*fn)(RopeArgs) = rope_any_kernel;
   if (vec) {

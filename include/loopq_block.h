@@ -88,7 +88,7 @@ typedef enum {
 
 /* The frequencies of a scaling as fp64 [rot_dim / 2] in host memory (host only).
  * base > 1; factor >= 1 (ignored by PLAIN); length > 0 and 0 <= low < high
- * (PARTS only); all finite.  rot_dim even, 2 .. 128 (from 4 on for BASE). */
+ * (PARTS only); all finite, the longer base of BASE too.  rot_dim even, 2 .. 128 (from 4 on for BASE). */
 int32_t loopq_rope_frequencies(int32_t scaling, int32_t rot_dim, double base, double factor, double length,
                                double low, double high, double* inv_freq_host);
 
@@ -103,7 +103,8 @@ int32_t loopq_rope(const void* x, int64_t ldx, int32_t dtype, int32_t tokens, in
  * and then, with v as it is, rounded to bf16 and written to the slab; q is turned
  * into q_out.  Token i of the n that cu gives row b (the last of its lens[b]
  * tokens, see loopq_kv_write) is at position lens[b] - n + i.  cu, k, v, dtype,
- * tokens as for loopq_kv_write: a token whose position has no page is dropped (its
+ * tokens as for loopq_kv_write (but rows of q, k and v from cu[rows] up to tokens
+ * may be read, without effect): a token whose position has no page is dropped (its
  * q is turned all the same).  q [tokens][heads_q][head_dim] in `dtype`, q_out the
  * same shape in q_dtype (bf16 queries suit loopq_attn_prefill), 16-byte aligned
  * rows ldq and ldqo elements apart; q_out may be q itself (the same address,
@@ -129,9 +130,11 @@ int32_t loopq_kv_write_rope(const loopq_kv_pool* pool_host, int32_t slab, const 
  * Products of x and A and of A x and B are formed from all bits of their factors
  * (of 2^-100 and more in magnitude), sums are fp32 in an order that depends on
  * the sizes only: a row's result does not depend on other rows' ids.  An infinity
- * or NaN in a row or an adapter reaches no row but its own.
+ * or NaN in a row or an adapter reaches no row but its own (there an infinity may
+ * end as NaN).
  * max_rank a multiple of 8 up to 128; K % 8 == 0, K <= 65536; N <= 2^20;
- * adapters <= 2^16; rows <= 2^20; ldx, ldy < 2^24.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank);
+ * adapters <= 2^16; rows <= 2^20; ldx < 2^24 (fp32: 2^23),
+ * ldy < 2^24.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank);
  * two calls that share one must not overlap. */
 int32_t loopq_adapter_workspace_bytes(int32_t rows, int32_t max_rank, size_t* bytes_host);
 int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t rows, int32_t K, int32_t N,

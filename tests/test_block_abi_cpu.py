@@ -185,6 +185,12 @@ def test_frequencies():
         pytest.approx(block.loopq_rope_frequencies(block.LOOPQ_ROPE_PLAIN, 64, 500000.0), rel=1e-14)
 
 
+def test_a_base_that_overflows_is_refused(lib):
+    with pytest.raises(loopq.LoopQError):
+        block.loopq_rope_frequencies(block.LOOPQ_ROPE_BASE, 4, 1e300, 1e10)
+    assert block.loopq_rope_frequencies(block.LOOPQ_ROPE_LINEAR, 4, 1e300, 1e10)[0] == 1e-10
+
+
 # ----------------------------------------------------------------- adapters
 
 def adapter(lib, **kw):
@@ -202,7 +208,7 @@ def adapter(lib, **kw):
     (dict(y=None), INVALID), (dict(ldx=56), INVALID), (dict(ldy=47), INVALID), (dict(x=FAKE + 8), ALIGNMENT), (dict(ldx=66), ALIGNMENT),
     (dict(ids=FAKE + MB + 2), ALIGNMENT), (dict(A=FAKE + 2 * MB + 8), ALIGNMENT), (dict(B=FAKE + 3 * MB + 8), ALIGNMENT),
     (dict(scales=FAKE + 4 * MB + 1), ALIGNMENT), (dict(ranks=FAKE + 5 * MB + 2), ALIGNMENT), (dict(y=FAKE + 6 * MB + 2), ALIGNMENT),
-    (dict(ldx=1 << 24), UNSUPPORTED), (dict(ldy=1 << 24), UNSUPPORTED), (dict(y=FAKE), INVALID), (dict(y=FAKE + 256), INVALID), (dict(ws=None), WORKSPACE), (dict(size=0), WORKSPACE), (dict(ws=FAKE + 7 * MB + 64), ALIGNMENT)])
+    (dict(ldx=1 << 23), UNSUPPORTED), (dict(dt=BF16, ldx=1 << 24), UNSUPPORTED), (dict(ldy=1 << 24), UNSUPPORTED), (dict(y=FAKE), INVALID), (dict(y=FAKE + 256), INVALID), (dict(ws=None), WORKSPACE), (dict(size=0), WORKSPACE), (dict(ws=FAKE + 7 * MB + 64), ALIGNMENT)])
 def test_adapter_arguments(lib, kw, want):
     assert adapter(lib, **kw) == want
 

@@ -177,17 +177,18 @@ def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
         assert torch.equal(one[mine], mixed[mine])
 
 
-@pytest.mark.parametrize("rows", [40, 300])
-def test_rows_far_apart(lq, rows):
+@pytest.mark.parametrize("rows, dtype", [(40, BF16), (300, BF16), (300, F32)])
+def test_rows_far_apart(lq, rows, dtype):
     """Row distances at the limit: a tile spans almost 2^31 bytes, the matrix much more."""
     rng = np.random.default_rng(rows)
     K, N, n, R, ld = 264, 68, 3, 16, (1 << 24) - 8
+    ldx = ld if dtype is BF16 else (1 << 23) - 8
     x, A, B, s, y = whole(rng, rows, K, N, n, R)
     ids = np.sort(rng.integers(-1, n, rows))
     want, _ = reference(x, ids, A, B, s, None, y)
-    xw = torch.empty((rows - 1) * ld + K, dtype=BF16, device="cuda").as_strided((rows, K), (ld, 1))
+    xw = torch.empty((rows - 1) * ldx + K, dtype=dtype, device="cuda").as_strided((rows, K), (ldx, 1))
     yw = torch.empty((rows - 1) * ld + N, device="cuda").as_strided((rows, N), (ld, 1))
-    xw.copy_(dev(x, BF16))
+    xw.copy_(dev(x, dtype))
     yw.copy_(dev(y))
     apply(xw, ids, dev(A, BF16), dev(B, BF16), dev(s, F32), yw)
     assert torch.equal(yw.double().cpu(), torch.from_numpy(want))

@@ -137,6 +137,18 @@ def test_rows_of_zeros_and_extremes(lq, rows, K):
     assert not out["y"][0].any() and not out["codes"][0].any() and not out["steps"][0].any()
 
 
+@pytest.mark.parametrize("rows,K", [(5, 64), (5, 2048), (700, 2560)])
+def test_codes_of_weights_that_are_not_finite(lq, rows, K):
+    """Finite rows, weights that make z infinite, NaN or overflow: codes and steps as loopq_quant_act has them from z."""
+    x, w = make(rows, K, torch.float32, 27), torch.ones(K, device="cuda")
+    w[3], w[35], w[36] = float("inf"), float("nan"), 3.4e38
+    y, codes, steps = torch.empty_like(x), torch.empty((rows, K), dtype=torch.int8, device="cuda"), torch.empty((rows, K // 32), device="cuda")
+    block.loopq_rms_norm(x, w, float(EPS), y=y, codes=codes, steps=steps, bits_a=8)
+    c2, s2 = torch.empty_like(codes), torch.empty_like(steps)
+    lq.loopq_quant_act(y, None, None, 1.0, 8, c2, s2)
+    assert torch.equal(codes, c2) and np.array_equal(f32(steps), f32(s2), equal_nan=True)
+
+
 @pytest.mark.parametrize("rows,K", [(6, 64), (6, 2048), (1200, 2560), (6, 6912), (6, 10560)])
 @pytest.mark.parametrize("rt", [torch.float32, torch.bfloat16])
 def test_rows_that_are_not_finite(lq, rows, K, rt):
