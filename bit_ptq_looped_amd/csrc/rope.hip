@@ -8,6 +8,9 @@
 // positions cost no precision, and sine and cosine of half turns (sincospif)
 // need no reduction of their own.  The work is bound by the bytes of the
 // tensors: the first heads' loads are issued before the position is looked up.
+// 8192 tokens of 32 heads of 128: bf16 28 us, fp32 53 (4.8 and 5.0 TB/s, a large
+// copy reaches 4.8); 16384 tokens of 40 heads into the cache, queries out in bf16:
+// 117 (5.2 TB/s); a single token 3.0, of which all but a fraction is the launch.
 //
 // The row of a token is found by a search of the wave, 64 probes of cu at once:
 // one trip to memory for up to 64 rows, two up to 4096.
@@ -188,92 +191,105 @@ __global__ __launch_bounds__(256) void rope_vec_kernel(RopeArgs a) {
   }
 }
 
-__device__ __forceinline__ float load1(const void* p, int64_t at, bool bf16) {
-  return bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[at]) : reinterpret_cast<const float*>(p)[at];
-}
-__device__ __forceinline__ void store1(void* p, int64_t at, float v, bool bf16) {
-  if (bf16) reinterpret_cast<uint16_t*>(p)[at] = (uint16_t)bf16x2_rne(v, v);
-  else reinterpret_cast<float*>(p)[at] = v;
-}
-
-// Any even rot_dim: lane i takes pair i of a head and elements rot_dim + i and
-// rot_dim + i + 64 of its rest, single elements side by side, U heads at a time.
+// Any even rot_dim: a lane takes eight elements of a head.  Pairs side by side lie
+// within them; halves rot_dim / 2 apart lie where no 16-byte access starts, so a
+// wave's heads pass through its part of LDS (nine places for eight elements, so that
+// 64 lanes a run apart hit 64 banks).  8192 tokens of 32 heads, bf16, 100 of 128
+// elements turned: 30 us (single elements a lane, in 2-byte accesses: 108).
+template <int D, int BF>
 __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
-  constexpr int U = 4;
+  constexpr int S = D / 8, HP = 64 / S;
+  __shared__ float row[4][64 * 9];
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t t = w / a.split;
   if (t >= a.tokens) return;
-  const int D = a.head_dim;
+  const int slot = lane % S, hl = lane / S, e0 = 8 * slot;
   const int h0 = (int)(w - t * a.split) * a.per;
   const int h1 = min(h0 + a.per, a.heads);
+  Eight<BF> x;
+  auto load = [&](int head) {
+    if (hl < HP && head < h1) {
+      int at;
+      const RopePart& p = a.part[part_of(a, head, &at)];
+      x.load(p.in, t * p.ld_in + (int64_t)at * D + e0);
+    }
+  };
+  load(h0 + hl);
   const Place pl = find_place(a, t, lane);
   if (pl.skip) return;
-  const bool pair = lane < a.rot / 2;
-  const int ea = a.pairs ? 2 * lane : lane, eb = a.pairs ? 2 * lane + 1 : lane + a.rot / 2;
-  float c = 0.0f, s = 0.0f;
-  if (pair) turn_of(a, pl.pos, lane, &c, &s);
-  for (int g = h0; g < h1; g += U) {
-    float x[U][4];
+  float cl = 0.0f, sl = 0.0f;
+  if (lane < a.rot / 2) turn_of(a, pl.pos, lane, &cl, &sl);
+  // element j becomes c x + s (the other of its pair), s with its sign
+  float c[8], s[8];
+  int other[8];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (g + j >= h1) break;
-      int at;
-      const int which = part_of(a, g + j, &at);
-      const RopePart& p = a.part[which];
-      const int64_t base = t * p.ld_in + (int64_t)at * D;
-      const int from = which == 2 ? 0 : a.rot;
-      if (which != 2 && pair) {
-        x[j][0] = load1(p.in, base + ea, a.in_bf16);
-        x[j][1] = load1(p.in, base + eb, a.in_bf16);
-      }
-      if (from + lane < D) x[j][2] = load1(p.in, base + from + lane, a.in_bf16);
-      if (from + lane + 64 < D) x[j][3] = load1(p.in, base + from + lane + 64, a.in_bf16);
-    }
+  for (int j = 0; j < 8; ++j) {
+    const int e = e0 + j, half = a.rot / 2;
+    const bool second = a.pairs ? j & 1 : e >= half;
+    const int i = a.pairs ? e >> 1 : second ? e - half : e;
+    const float sj = __shfl(sl, i & 63);
+    c[j] = __shfl(cl, i & 63);
+    s[j] = second ? sj : -sj;
+    const int o = e >= a.rot ? e : second ? e - half : e + half;
+    other[j] = hl * S * 9 + o + (o >> 3);
+  }
+  float* mine = row[threadIdx.x >> 6];
+  for (int head = h0 + hl; head - hl < h1; head += HP) {
+    float u[8], v[8];
+    x.floats(u);
+    load(head + HP);
+    if (a.pairs) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (g + j >= h1) break;
-      int at;
-      const int which = part_of(a, g + j, &at);
-      void* d;
-      int64_t base = 0;
-      bool bf16 = true;
-      if (which == 0) {
-        d = a.part[0].out;
-        base = t * a.part[0].ld_out + (int64_t)at * D;
-        bf16 = a.part[0].out_bf16;
-      } else {
-        if (!pl.paged) continue;
-        d = pl.dst + ((int64_t)at << a.page_shift) * D + (which == 2 ? a.plane : 0);
+      for (int j = 0; j < 8; ++j) v[j] = u[j ^ 1];
+    } else {  // the other lanes' elements: LDS operations of a wave complete in order
+      if (hl < HP) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mine[9 * lane + j] = u[j];
       }
-      const int from = which == 2 ? 0 : a.rot;
-      if (which != 2 && pair) {
-        store1(d, base + ea, x[j][0] * c - x[j][1] * s, bf16);
-        store1(d, base + eb, x[j][1] * c + x[j][0] * s, bf16);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (hl < HP) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = mine[other[j]];
       }
-      if (from + lane < D) store1(d, base + from + lane, x[j][2], bf16);
-      if (from + lane + 64 < D) store1(d, base + from + lane + 64, x[j][3], bf16);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    if (hl >= HP || head >= h1) continue;
+    int at;
+    const int which = part_of(a, head, &at);
+    if (which != 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = e0 + j < a.rot ? u[j] * c[j] + v[j] * s[j] : u[j];
+    }
+    if (which == 0) store8(a.part[0].out, t * a.part[0].ld_out + (int64_t)at * D + e0, u, a.part[0].out_bf16);
+    else if (pl.paged) store8(pl.dst + ((int64_t)at << a.page_shift) * D + (which == 2 ? a.plane : 0), e0, u, true);
   }
 }
 
 }  // namespace
 
 hipError_t launch_rope(RopeArgs a, hipStream_t s) {
+  // where the halves of pairs start at 16 bytes too, LDS is not needed: 8192 tokens of 27
+  // heads of 96 in bf16 take 16.4 us (through LDS 20.3), of 32 of 128 in fp32 53 (60)
   const bool vec = a.rot % 16 == 0;
-  const int step = vec ? 64 / (a.head_dim / 16) : 4;  // heads of a pass
+  const int step = 64 / (a.head_dim / (vec ? 16 : 8));  // heads of a pass
   const int passes = (a.heads + step - 1) / step;
-  // a token's heads are shared out among waves while there are few tokens
+  // a token's heads are shared out among waves while there are few tokens: 4096 waves are
+  // four a SIMD, and eight find room
   const int want = (int)((4096 + (int64_t)a.tokens - 1) / a.tokens);
   int split = want < passes ? want : passes;
   a.per = (passes + split - 1) / split * step;
   a.split = (a.heads + a.per - 1) / a.per;
   const unsigned grid = (unsigned)(((int64_t)a.tokens * a.split + 3) / 4);
-  void (*fn)(RopeArgs) = rope_any_kernel;
+  void (*fn)(RopeArgs);
   if (vec) {
     if (a.head_dim == 64) fn = a.in_bf16 ? rope_vec_kernel<64, 1> : rope_vec_kernel<64, 0>;
     else if (a.head_dim == 96) fn = a.in_bf16 ? rope_vec_kernel<96, 1> : rope_vec_kernel<96, 0>;
     else fn = a.in_bf16 ? rope_vec_kernel<128, 1> : rope_vec_kernel<128, 0>;
+  } else {
+    if (a.head_dim == 64) fn = a.in_bf16 ? rope_any_kernel<64, 1> : rope_any_kernel<64, 0>;
+    else if (a.head_dim == 96) fn = a.in_bf16 ? rope_any_kernel<96, 1> : rope_any_kernel<96, 0>;
+    else fn = a.in_bf16 ? rope_any_kernel<128, 1> : rope_any_kernel<128, 0>;
   }
   fn<<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
