@@ -4,6 +4,8 @@
 //
 // Two launches: the first forms z (fp32, in the workspace), the second adds its
 // product to y.  Rows without an adapter cost their id's read.
+#include <type_traits>
+
 #include "block_internal.h"
 #include "quant_core.h"
 
@@ -194,7 +196,7 @@ hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
 
 constexpr int kTile = 64;    // tokens of a shrink work-group, 16 a wave
 constexpr int kTokens = 128; // tokens of an expand work-group, 32 a wave
-constexpr int kFew = 6;
+constexpr int kFew = 3;
 constexpr int kMaxSplits = 16;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -222,6 +224,48 @@ struct Adapters {
 // lane without a part in one names the place kNone, past the end: the load gives 0
 // and the store is dropped, without a branch around each.
 constexpr uint32_t kNone = 0x80000000u;
+
+// Tokens in any order are put in the order of their adapters, segment by segment, so
+// that a wave meets few of them.  Every work-group of a segment does this for itself.
+constexpr int kSegment = 1024;
+constexpr int kRuns = 32;
+constexpr uint32_t kNoAdapter = 1u << 16;
+
+// key: adapter (kNoAdapter: none) * 1024 + place in the segment, ~0 past the last row.
+// False, and nothing written, where ids change at most kRuns times from row to row.
+__device__ __forceinline__ bool order_segment(const AdapterArgs& a, int64_t base, uint32_t* key, int* runs_of) {
+  constexpr int E = kSegment / 256;
+  const int tid = threadIdx.x, i0 = E * tid;
+  const int count = (int)min((int64_t)kSegment, a.rows - base);
+  int id[E + 1];  // of the place before a thread's first one and of its own
+#pragma unroll
+  for (int e = 0; e <= E; ++e) id[e] = adapter_of(a, base + min(max(i0 + e - 1, 0), count - 1));
+  int runs = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) runs += __popcll(__ballot(id[e] != id[e + 1]));
+  if ((tid & 63) == 0) runs_of[tid >> 6] = runs;
+  __syncthreads();
+  if (runs_of[0] + runs_of[1] + runs_of[2] + runs_of[3] <= kRuns) return false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = i0 + e;
+    key[i] = i < count ? (id[e + 1] < 0 ? kNoAdapter : (uint32_t)id[e + 1]) * kSegment + i : ~0u;
+  }
+  __syncthreads();
+  for (int k = 2; k <= kSegment; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+#pragma unroll
+      for (int e = 0; e < kSegment / 512; ++e) {
+        const int p = tid + 256 * e, i = 2 * (p & ~(j - 1)) + (p & (j - 1));
+        const uint32_t u = key[i], v = key[i + j];
+        const bool up = (i & k) == 0;
+        key[i] = up ? min(u, v) : max(u, v);
+        key[i + j] = up ? max(u, v) : min(u, v);
+      }
+      __syncthreads();
+    }
+  return true;
+}
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
@@ -269,14 +313,28 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int64_t m0 = (int64_t)blockIdx.x * kTile;
-  const int id = m0 + lane < a.rows ? adapter_of(a, m0 + lane) : -1;
+  // the token of this lane's place
+  int64_t base = m0, row = m0 + lane;
+  int id = row < a.rows ? adapter_of(a, row) : -1;
+  if (a.sort) {
+    uint32_t* key = reinterpret_cast<uint32_t*>(sx);
+    static_assert(sizeof(sx) >= kSegment * 4 && sizeof(sw) >= 16, "the keys of a segment fit");
+    base = m0 / kSegment * kSegment;
+    if (order_segment(a, base, key, reinterpret_cast<int*>(sw))) {
+      const uint32_t k = key[(int)(m0 - base) + lane];
+      row = base + k % kSegment;
+      id = k / kSegment < kNoAdapter ? (int)(k / kSegment) : -1;
+    }
+  }
+  if (blockIdx.y == 0 && wave == 0 && m0 + lane < a.rows) a.order[m0 + lane] = int2{(int)row, id};
   Adapters todo(id, ~0ull);
   if (todo.left == 0) return;
   int few = 0;
   for (Adapters all = todo; all.left && few <= kFew; ++few) all.next();
   const int chunks = (a.K + KC - 1) / KC;
   const int c0 = (uint32_t)chunks * blockIdx.y / gridDim.y, c1 = (uint32_t)chunks * (blockIdx.y + 1) / gridDim.y;
-  const auto xr = resource(reinterpret_cast<const char*>(a.x) + m0 * a.ldx * item, (kTile - 1) * a.ldx * item + a.K * item);
+  const auto xr = resource(reinterpret_cast<const char*>(a.x) + base * a.ldx * item, ((a.sort ? kSegment : kTile) - 1) * a.ldx * item + a.K * item);
+  const uint32_t row_at = (uint32_t)((row - base) * a.ldx * item);
   const int my_id = __shfl(id, 16 * wave + li);  // the token of this lane's results
   float* z = a.z + ((int64_t)blockIdx.y * a.rows + m0 + 16 * wave + li) * a.R;
   v4f acc[RT];
@@ -295,8 +353,12 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
 
   if (few <= kFew) {
     int xid[4];
+    uint32_t xat[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) xid[i] = __shfl(id, (int)(threadIdx.x >> 4) + 16 * i);
+    for (int i = 0; i < 4; ++i) {
+      xid[i] = __shfl(id, (int)(threadIdx.x >> 4) + 16 * i);
+      xat[i] = __shfl(row_at, (int)(threadIdx.x >> 4) + 16 * i);
+    }
     while (todo.left) {
       const int ad = todo.next(), rank = wave_rank_of(a, ad);
       const auto wr = resource(a.A + (int64_t)ad * a.R * a.K, (int64_t)rank * a.K * 2);  // rows from the rank on lie outside
@@ -308,7 +370,7 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
         const int kx = c * KC + (int)(threadIdx.x & 15) * (16 / item);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s.x[i] = load16(xr, xid[i] == ad && kx < a.K && c < c1 ? (uint32_t)((((int)(threadIdx.x >> 4) + 16 * i) * a.ldx + kx) * item) : kNone);
+          s.x[i] = load16(xr, xid[i] == ad && kx < a.K && c < c1 ? xat[i] + (uint32_t)(kx * item) : kNone);
         const int kw = c * KC + (int)(threadIdx.x % WL) * 8;
 #pragma unroll
         for (int i = 0; i < WN; ++i) {
@@ -361,7 +423,7 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
     int ad, rank, k0;
   };
   Adapters own(my_id, 0xFFFFull);
-  const uint32_t xat = (uint32_t)((16 * wave + li) * a.ldx * item);
+  const uint32_t xat = __shfl(row_at, 16 * wave + li);
   const int k_begin = c0 * KC, k_end = min(a.K, c1 * KC);
   if (own.left == 0 || k_begin >= k_end) return;
   int ad = own.next(), rank = wave_rank_of(a, ad), k0 = k_begin;
@@ -404,7 +466,7 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
 }
 
 // The splits' sums of z, added in their order, as three bf16 planes: [row][R / 8][3][8].
-// A thread takes eight ranks of a token; ranks that its adapter does not have are 0.
+// A thread takes eight ranks of a place's token; ranks that its adapter does not have are 0.
 // (Read by the next kernel itself, 16 splits of 1500 tokens cost it 9 us in each of 40
 // stripes of N, this launch 3.)
 __global__ __launch_bounds__(256) void join_kernel(AdapterArgs a, int splits) {
@@ -412,7 +474,7 @@ __global__ __launch_bounds__(256) void join_kernel(AdapterArgs a, int splits) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = i / per;
   if (m >= a.rows) return;
-  const int id = adapter_of(a, m);
+  const int id = a.order[m].y;
   if (id < 0) return;
   const int j = (int)(i - m * per) * 8, rank = rank_of(a, id);
   float v[8] = {};
@@ -450,15 +512,22 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
   constexpr int BN = NB * BL / 256;      // loads of a thread
   static_assert(NB * BL % 256 == 0 || NB * BL == 128, "a block is whole loads of the work-group");
   __shared__ __attribute__((aligned(16))) char sb[NB * BS];
+  __shared__ __attribute__((aligned(16))) uint32_t sy[kTokens];  // where the tokens' rows of y begin
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 31, lh = lane >> 5;
   const int group = blockIdx.x / stripes;
   const int64_t t0 = (int64_t)group * kTokens;
   // ids of all the tokens (two a lane) decide the form, those of this wave's 32 the work
-  const int id_a = t0 + lane < a.rows ? adapter_of(a, t0 + lane) : -1;
-  const int id_b = t0 + 64 + lane < a.rows ? adapter_of(a, t0 + 64 + lane) : -1;
+  const int2 first = t0 + lane < a.rows ? a.order[t0 + lane] : int2{0, -1};
+  const int2 second = t0 + 64 + lane < a.rows ? a.order[t0 + 64 + lane] : int2{0, -1};
+  const int id_a = first.y, id_b = second.y;
   const int64_t m0 = t0 + 32 * wave;
+  const int64_t base = a.sort ? t0 / kSegment * kSegment : m0;
+  const int row = __shfl(wave < 2 ? first.x : second.x, 32 * (wave & 1) + li);
+  if (lane < 32) sy[32 * wave + li] = (uint32_t)((row - base) * a.ldy * 4);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // read by this wave only
   const int id = __shfl(wave < 2 ? id_a : id_b, 32 * (wave & 1) + li);
+  const bool straight = __ballot((id_a >= 0 && first.x != t0 + lane) || (id_b >= 0 && second.x != t0 + 64 + lane)) == 0;
   Adapters lower(id_a, ~0ull), upper(id_b, ~0ull);
   if (lower.left == 0 && upper.left == 0) return;
   int few = 0;
@@ -471,7 +540,7 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
     for (; u.left && few <= kFew; ++few) u.next();
   }
   const int n_begin = (blockIdx.x - group * stripes) * stripe, n_end = min(a.N, n_begin + stripe);
-  const auto yr = resource(a.y + m0 * a.ldy, 31 * a.ldy * 4 + (int64_t)a.N * 4);
+  const auto yr = resource(a.y + base * a.ldy, ((a.sort ? kSegment : 32) - 1) * a.ldy * 4 + (int64_t)a.N * 4);
   // z of the wave's tokens
   u32x4 z[RS][3];
   auto load_z = [&]() {
@@ -484,31 +553,41 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
       for (int p = 0; p < 3; ++p) z[t][p] = load16(zr, at + 16 * p);
     }
   };
-  // Element e of a result is token 8 (e / 4) + 4 lh + e % 4, output li: the lane's place
-  // and a row distance of the wave.  Tokens of other adapters are masked unless all 32
-  // are this one's.
+  // Element e of a result is token 8 (e / 4) + 4 lh + e % 4, output li.  Tokens of other
+  // adapters are masked.
   // (lane_tokens: bit 8 (e / 4) + e % 4 is the lane's token e)
   auto lane_tokens = [&](uint64_t is) { return lh ? (uint32_t)(is >> 4) : (uint32_t)is; };
   uint32_t mine_of = 0;
   bool whole = false;
-  const uint32_t lane_at = (uint32_t)(4 * lh * a.ldy * 4);
   auto set_tokens = [&](uint64_t is) {
     mine_of = lane_tokens(is);
     whole = is == ~0ull;
     return is != 0;
   };
-  auto row_at = [&](int e) { return (int)((8 * (e / 4) + e % 4) * a.ldy * 4); };
-  auto load_y = [&](v16f& old, int n) {
-    const uint32_t at = n + li < n_end ? lane_at + 4u * (n + li) : kNone;
+  // f(e, place of element e in y, the part of it that is the wave's).  Tokens of a tile that
+  // is straight lie a row apart, those of another where sy says.
+  const uint32_t lane_at = (uint32_t)((m0 - base + 4 * lh) * a.ldy * 4);
+  auto each_y = [&](auto straight, int n, auto f) {
+    const uint32_t at = 4u * (n + li), mine = n + li < n_end ? mine_of : 0u;
+    if constexpr (straight) {
+      const uint32_t to = n + li < n_end ? lane_at + at : kNone;
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, whole || (mine_of & (1u << (8 * (e / 4) + e % 4))) ? at : kNone, row_at(e), 0));
+      for (int e = 0; e < 16; ++e)
+        f(e, whole || (mine_of & (1u << (8 * (e / 4) + e % 4))) ? to : kNone, (int)((8 * (e / 4) + e % 4) * a.ldy * 4));
+      return;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const u32x4 r = *reinterpret_cast<const u32x4*>(sy + 32 * wave + 8 * g + 4 * lh);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f(4 * g + i, mine & (1u << (8 * g + i)) ? r[i] + at : kNone, 0);
+    }
   };
-  auto store_y = [&](const v16f& old, const v16f& v, int n) {
-    const uint32_t at = n + li < n_end ? lane_at + 4u * (n + li) : kNone;
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + v[e]), yr, whole || (mine_of & (1u << (8 * (e / 4) + e % 4))) ? at : kNone, row_at(e), 0);
+  auto load_y = [&](auto straight, v16f& old, int n) {
+    each_y(straight, n, [&](int e, uint32_t at, int wave_at) { old[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(yr, at, wave_at, 0)); });
+  };
+  auto store_y = [&](auto straight, const v16f& old, const v16f& v, int n) {
+    each_y(straight, n, [&](int e, uint32_t at, int wave_at) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(old[e] + v[e]), yr, at, wave_at, 0); });
   };
   // ranks that an adapter does not have among a lane's eight of step t
   auto cut = [&](u32x4 v, int t, int rank) {
@@ -526,10 +605,10 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
 #pragma unroll
       for (int t = 0; t < RS; ++t) acc = mm32(z[t][p], b[t], acc);
     mfma_settle_before_join();
-    store_y(old, acc, n);
+    store_y(std::true_type{}, old, acc, n);
   };
 
-  if (few <= kFew) {
+  if (few <= kFew && straight) {
     bool have_z = false;
     while (lower.left || upper.left) {
       int ad;
@@ -568,8 +647,8 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
         continue;
       }
       v16f old[2];
-      load_y(old[0], n_begin);
-      load_y(old[1], n_begin + 32);
+      load_y(std::true_type{}, old[0], n_begin);
+      load_y(std::true_type{}, old[1], n_begin + 32);
       if (!have_z) load_z();
       have_z = true;
       for (int n0 = n_begin; n0 < n_end; n0 += NB) {
@@ -585,7 +664,7 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
             for (int t = 0; t < RS; ++t) bo[t] = cut(bo[t], t, rank);
           }
           multiply(bo, old[h], n0 + 32 * h);
-          load_y(old[h], n0 + NB + 32 * h);
+          load_y(std::true_type{}, old[h], n0 + NB + 32 * h);
         }
       }
     }
@@ -604,8 +683,8 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
   };
   for (int n = n_begin; n < n_end; n += NB) {
     v16f old[2], got[2] = {};
-    load_y(old[0], n);
-    load_y(old[1], n + 32);
+    load_y(std::false_type{}, old[0], n);
+    load_y(std::false_type{}, old[1], n + 32);
     Adapters left = own;
     // the next adapter's part of B; always the same number of loads, so that the wait for
     // one part leaves the next one's under way
@@ -649,8 +728,8 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
       pick(p1);
       if (p0.ad < 0) break;
     }
-    store_y(old[0], got[0], n);
-    store_y(old[1], got[1], n + 32);
+    store_y(std::false_type{}, old[0], got[0], n);
+    store_y(std::false_type{}, old[1], got[1], n + 32);
   }
 }
 
@@ -694,16 +773,22 @@ hipError_t launch_tiles(const AdapterArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// z of each split of K (at most what splits_for gives for any K), and its planes
+// z of each split of K (at most what splits_for gives for any K), its planes, the order
 static size_t sums_bytes(int64_t rows, int max_rank) {
   return (size_t)(splits_for(rows > 0 ? rows : 1, 1 << 30) * rows * max_rank * 4 + 255) / 256 * 256;
 }
+static size_t planes_bytes(int64_t rows, int max_rank) { return (size_t)(rows * max_rank * 6 + 255) / 256 * 256; }
 size_t adapter_workspace_bytes(int64_t rows, int max_rank) {
-  return sums_bytes(rows, max_rank) + (size_t)(rows * max_rank * 6 + 255) / 256 * 256;
+  return sums_bytes(rows, max_rank) + planes_bytes(rows, max_rank) + (size_t)(rows * 8 + 255) / 256 * 256;
 }
 
 hipError_t launch_adapter(AdapterArgs a, hipStream_t s) {
-  a.planes = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(a.z) + sums_bytes(a.rows, a.R));
+  char* at = reinterpret_cast<char*>(a.z) + sums_bytes(a.rows, a.R);
+  a.planes = reinterpret_cast<uint16_t*>(at);
+  a.order = reinterpret_cast<int2*>(at + planes_bytes(a.rows, a.R));
+  // a segment's rows of x and of y lie within 2^31 bytes, but for matrices of far wider rows
+  const int64_t most = (int64_t)1 << 31, item = a.x_bf16 ? 2 : 4;
+  a.sort = (kSegment - 1) * a.ldx * item + a.K * item < most && (kSegment - 1) * a.ldy * 4 + (int64_t)a.N * 4 < most;
   return a.rows <= 256 ? launch_rows(a, s) : launch_tiles(a, s);
 }
 

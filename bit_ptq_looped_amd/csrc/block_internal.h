@@ -71,8 +71,10 @@ struct AdapterArgs {
   int adapters, R;
   float* y;
   int64_t ldy;
+  bool sort;             // (by the launcher) tokens of a segment may be put in order
   float* z;              // workspace: [splits][rows][R]
-  uint16_t* planes;      // behind it: bf16 [rows][R / 8][3][8] (set by the launcher)
+  uint16_t* planes;      // behind it: bf16 [rows][R / 8][3][8] (by the launcher)
+  int2* order;           // behind them: row and adapter (or -1) of each place [rows] (by the launcher)
 };
 size_t adapter_workspace_bytes(int64_t rows, int max_rank);
 hipError_t launch_adapter(AdapterArgs a, hipStream_t s);

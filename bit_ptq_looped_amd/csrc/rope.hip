@@ -9,7 +9,8 @@
 // need no reduction of their own.  The work is bound by the bytes of the
 // tensors: the first heads' loads are issued before the position is looked up.
 // 8192 tokens of 32 heads of 128: bf16 28 us, fp32 53 (4.8 and 5.0 TB/s, a large
-// copy reaches 4.8); 16384 tokens of 40 heads into the cache, queries out in bf16:
+// copy reaches 4.8); 16384 tokens of 16 heads each of fp32 queries, keys and values,
+// keys and values into the cache, queries out in bf16:
 // 117 (5.2 TB/s); a single token 3.0, of which all but a fraction is the launch.
 //
 // The row of a token is found by a search of the wave, 64 probes of cu at once:
