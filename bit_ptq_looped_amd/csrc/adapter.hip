@@ -229,41 +229,58 @@ constexpr uint32_t kNone = 0x80000000u;
 // that a wave meets few of them.  Every work-group of a segment does this for itself.
 constexpr int kSegment = 1024;
 constexpr int kRuns = 32;
-constexpr uint32_t kNoAdapter = 1u << 16;
-
-// key: adapter (kNoAdapter: none) * 1024 + place in the segment, ~0 past the last row.
-// False, and nothing written, where ids change at most kRuns times from row to row.
-__device__ __forceinline__ bool order_segment(const AdapterArgs& a, int64_t base, uint32_t* key, int* runs_of) {
+// key: the place in the segment, and above its ten bits the adapter (a.adapters: none, or
+// past the last row).  False, and nothing written, where ids change at most kRuns times from
+// row to row.  Sorted by one bit of the adapter after the other, stably, four places a thread.
+// share: 20 ints.
+__device__ __forceinline__ bool order_segment(const AdapterArgs& a, int64_t base, uint32_t* key, int* share) {
   constexpr int E = kSegment / 256;
-  const int tid = threadIdx.x, i0 = E * tid;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int count = (int)min((int64_t)kSegment, a.rows - base);
-  int id[E + 1];  // of the place before a thread's first one and of its own
-#pragma unroll
-  for (int e = 0; e <= E; ++e) id[e] = adapter_of(a, base + min(max(i0 + e - 1, 0), count - 1));
-  int runs = 0;
-#pragma unroll
-  for (int e = 0; e < E; ++e) runs += __popcll(__ballot(id[e] != id[e + 1]));
-  if ((tid & 63) == 0) runs_of[tid >> 6] = runs;
-  __syncthreads();
-  if (runs_of[0] + runs_of[1] + runs_of[2] + runs_of[3] <= kRuns) return false;
+  int id[E], before[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int i = i0 + e;
-    key[i] = i < count ? (id[e + 1] < 0 ? kNoAdapter : (uint32_t)id[e + 1]) * kSegment + i : ~0u;
+    const int i = 256 * e + tid;
+    id[e] = adapter_of(a, base + min(i, count - 1));
+    before[e] = adapter_of(a, base + min(max(i - 1, 0), count - 1));
   }
-  __syncthreads();
-  for (int k = 2; k <= kSegment; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
+  int runs = 0;
 #pragma unroll
-      for (int e = 0; e < kSegment / 512; ++e) {
-        const int p = tid + 256 * e, i = 2 * (p & ~(j - 1)) + (p & (j - 1));
-        const uint32_t u = key[i], v = key[i + j];
-        const bool up = (i & k) == 0;
-        key[i] = up ? min(u, v) : max(u, v);
-        key[i + j] = up ? max(u, v) : min(u, v);
-      }
-      __syncthreads();
+  for (int e = 0; e < E; ++e) runs += __popcll(__ballot(id[e] != before[e]));
+  if (lane == 0) share[16 + wave] = runs;
+  __syncthreads();
+  if (share[16] + share[17] + share[18] + share[19] <= kRuns) return false;
+  uint32_t v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = 256 * e + tid;
+    v[e] = (uint32_t)(i < count && id[e] >= 0 ? id[e] : a.adapters) * kSegment + i;
+  }
+  for (uint32_t bit = kSegment; bit <= (uint32_t)a.adapters * kSegment; bit *= 2) {
+    uint64_t zeros[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      zeros[e] = __ballot(!(v[e] & bit));
+      if (lane == 0) share[4 * e + wave] = __popcll(zeros[e]);
     }
+    __syncthreads();
+    int all = 0, at[E];
+#pragma unroll
+    for (int q = 0; q < 4 * E; ++q) {
+      if (q % 4 == 0) at[q / 4] = all;
+      const int n = share[q];
+      if (q % 4 < wave) at[q / 4] += n;
+      all += n;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int z = at[e] + __popcll(zeros[e] & ((1ull << lane) - 1));
+      key[v[e] & bit ? all + 256 * e + tid - z : z] = v[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = key[256 * e + tid];
+  }
   return true;
 }
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int64_t bytes) {
@@ -318,12 +335,12 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(AdapterArgs a) {
   int id = row < a.rows ? adapter_of(a, row) : -1;
   if (a.sort) {
     uint32_t* key = reinterpret_cast<uint32_t*>(sx);
-    static_assert(sizeof(sx) >= kSegment * 4 && sizeof(sw) >= 16, "the keys of a segment fit");
+    static_assert(sizeof(sx) >= kSegment * 4 && sizeof(sw) >= 80, "the keys of a segment fit");
     base = m0 / kSegment * kSegment;
     if (order_segment(a, base, key, reinterpret_cast<int*>(sw))) {
       const uint32_t k = key[(int)(m0 - base) + lane];
       row = base + k % kSegment;
-      id = k / kSegment < kNoAdapter ? (int)(k / kSegment) : -1;
+      id = (int)(k / kSegment) < a.adapters ? (int)(k / kSegment) : -1;
     }
   }
   if (blockIdx.y == 0 && wave == 0 && m0 + lane < a.rows) a.order[m0 + lane] = int2{(int)row, id};
@@ -789,7 +806,11 @@ hipError_t launch_adapter(AdapterArgs a, hipStream_t s) {
   // a segment's rows of x and of y lie within 2^31 bytes, but for matrices of far wider rows
   const int64_t most = (int64_t)1 << 31, item = a.x_bf16 ? 2 : 4;
   a.sort = (kSegment - 1) * a.ldx * item + a.K * item < most && (kSegment - 1) * a.ldy * 4 + (int64_t)a.N * 4 < most;
-  return a.rows <= 256 ? launch_rows(a, s) : launch_tiles(a, s);
+  // Few rows go one by one: tiles cost 14 us (in any order 20 and more) before they do
+  // anything, rows what they read.  rank 16, K and N of 2560, one by one and in tiles:
+  // 400 rows of 4 adapters 12 and 16 us, 600 of 32 in any order 17 and 24; rank 64, N of
+  // 6912: 160 rows 21 and 24, 256 29 and 18, 400 of 32 in any order 48 and 50.
+  return (int64_t)a.rows * (a.K + a.N) <= 5 << 19 ? launch_rows(a, s) : launch_tiles(a, s);
 }
 
 }  // namespace loopq

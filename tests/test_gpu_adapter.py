@@ -65,7 +65,11 @@ SIZES = [  # rows, K, N, adapters, max_rank
     (1, 8, 1, 1, 8), (1, 2048, 6144, 4, 16), (3, 520, 70, 2, 24), (16, 1024, 333, 5, 8), (17, 2560, 260, 3, 40),
     (48, 2560, 512, 32, 16), (64, 136, 129, 7, 128), (65, 384, 192, 4, 64), (100, 6912, 256, 8, 32), (129, 640, 68, 2, 72),
     (500, 2048, 1000, 6, 16), (700, 5632, 130, 3, 48), (1031, 264, 260, 40, 8), (2100, 512, 515, 5, 128), (5000, 96, 64, 3, 16),
-    (257, 8, 1, 3, 8), (300, 136, 77, 2, 24), (400, 520, 200, 20, 64), (320, 1032, 130, 9, 128), (600, 2048, 65, 70, 32), (1200, 304, 260, 30, 48)]
+    (257, 8, 1, 3, 8), (300, 136, 77, 2, 24), (400, 520, 200, 20, 64), (320, 1032, 130, 9, 128), (600, 2048, 65, 70, 32), (1200, 304, 260, 30, 48),
+    # in tiles: rows (K + N) of 5 2^19 and more
+    (257, 8, 10400, 3, 8), (300, 136, 8800, 2, 24), (400, 6520, 200, 20, 64), (320, 8200, 130, 9, 128), (600, 4360, 65, 70, 32),
+    (1200, 304, 1999, 30, 48), (5000, 456, 77, 3, 16), (2100, 1024, 515, 5, 128), (40000, 8, 64, 200, 8), (3000, 640, 257, 1500, 8),
+    (200, 13200, 33, 3, 72), (20, 64, 140000, 2, 16), (1031, 2560, 260, 40, 8)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -110,7 +114,8 @@ def test_real_numbers(lq, rows, K, N, n, R, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("rows,K,N,n,R", [(20, 512, 300, 4, 16), (200, 512, 320, 4, 64), (900, 768, 130, 4, 24)])
+@pytest.mark.parametrize("rows,K,N,n,R", [(20, 512, 300, 4, 16), (200, 512, 320, 4, 64), (900, 768, 130, 4, 24), (900, 2904, 130, 4, 24),
+                                             (300, 512, 8400, 4, 64), (2700, 968, 64, 30, 16)])
 def test_what_is_not_finite_stays_with_its_rows(lq, rows, K, N, n, R, dtype):
     rng = np.random.default_rng(rows)
     x, A, B, s, y = whole(rng, rows, K, N, n, R)
@@ -137,7 +142,7 @@ def test_what_is_not_finite_stays_with_its_rows(lq, rows, K, N, n, R, dtype):
     assert np.array_equal(got[fine], want[fine], equal_nan=True)
 
 
-@pytest.mark.parametrize("rows,K,N,n,R", [(7, 264, 131, 3, 16), (300, 512, 515, 3, 32), (1500, 520, 66, 3, 8)])
+@pytest.mark.parametrize("rows,K,N,n,R", [(7, 264, 131, 3, 16), (300, 512, 515, 3, 32), (1500, 520, 66, 3, 8), (300, 512, 8515, 3, 32), (1500, 1720, 66, 3, 8)])
 def test_strides_and_rows_without_an_adapter(lq, rows, K, N, n, R):
     """Columns of wider rows, odd distances of y, and nothing written but rows with an adapter."""
     rng = np.random.default_rng(rows)
@@ -160,7 +165,8 @@ def test_strides_and_rows_without_an_adapter(lq, rows, K, N, n, R):
 
 
 @pytest.mark.parametrize("rows,K,N,n,R", [(9, 1024, 300, 4, 16), (260, 1024, 300, 4, 64), (1300, 640, 100, 8, 16), (700, 2048, 300, 12, 64),
-                                             (300, 640, 130, 9, 128), (1000, 1024, 68, 40, 24)])
+                                             (300, 640, 130, 9, 128), (1000, 1024, 68, 40, 24), (1300, 1960, 100, 8, 16), (700, 2048, 1800, 12, 64),
+                                             (300, 640, 8130, 9, 128), (1100, 2408, 68, 40, 24)])
 def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
     rng = np.random.default_rng(rows)
     x, A, B = dev(rng.standard_normal((rows, K))), dev(rng.standard_normal((n, R, K)), BF16), dev(rng.standard_normal((n, N, R)), BF16)
@@ -177,14 +183,14 @@ def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
         assert torch.equal(one[mine], mixed[mine])
 
 
-@pytest.mark.parametrize("rows, dtype", [(40, BF16), (300, BF16), (300, F32)])
-def test_rows_far_apart(lq, rows, dtype):
+@pytest.mark.parametrize("rows, dtype, N", [(40, BF16, 68), (300, BF16, 8600), (300, F32, 8600)])
+def test_rows_far_apart(lq, rows, dtype, N):
     """Row distances at the limit: a tile spans almost 2^31 bytes, the matrix much more."""
     rng = np.random.default_rng(rows)
-    K, N, n, R, ld = 264, 68, 3, 16, (1 << 24) - 8
+    K, n, R, ld = 264, 3, 16, (1 << 24) - 8
     ldx = ld if dtype is BF16 else (1 << 23) - 8
     x, A, B, s, y = whole(rng, rows, K, N, n, R)
-    ids = np.sort(rng.integers(-1, n, rows))
+    ids = rng.integers(-1, n, rows)
     want, _ = reference(x, ids, A, B, s, None, y)
     xw = torch.empty((rows - 1) * ldx + K, dtype=dtype, device="cuda").as_strided((rows, K), (ldx, 1))
     yw = torch.empty((rows - 1) * ld + N, device="cuda").as_strided((rows, N), (ld, 1))
@@ -198,13 +204,13 @@ def test_no_rows_and_no_adapters(lq):
     A, B, s = dev(np.ones((2, 8, 16)), BF16), dev(np.ones((2, 5, 8)), BF16), dev(np.ones(2), F32)
     y = torch.zeros((0, 5), device="cuda")
     apply(torch.zeros((0, 16), device="cuda"), [], A, B, s, y)
-    for rows in (3, 400):
+    for rows in (3, 400, 130000):
         y = torch.full((rows, 5), float("nan"), device="cuda")
         apply(torch.zeros((rows, 16), device="cuda"), [-1] * rows, A, B, s, y)
         assert y.isnan().all()
 
 
-@pytest.mark.parametrize("rows", [6, 400])
+@pytest.mark.parametrize("rows", [6, 400, 2700])
 def test_on_a_stream_and_in_a_graph(lq, rows):
     rng = np.random.default_rng(rows)
     K, N, n, R = 768, 260, 4, 16
