@@ -76,8 +76,11 @@ def _types():
 
 def _on(t, stream):
     """The stream of a call whose first tensor is t: the current device's, where t has to live."""
-    if t.get_device() != _torch._C._cuda_getDevice():
+    index = t.get_device()
+    if index != _torch._C._cuda_getDevice():
         raise ValueError("the tensors' device must be the current one")
+    if stream is None and loopq._raw_stream is not None:
+        return loopq._raw_stream(index)
     return _stream(stream)
 
 

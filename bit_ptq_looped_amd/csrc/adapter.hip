@@ -2,8 +2,14 @@
 // (include/loopq_block.h has the definitions):
 //   z_m = scale_a A_a x_m,  y_m += B_a z_m,  a = ids[m].
 //
-// Two launches: the first forms z (fp32, in the workspace), the second adds its
-// product to y.  Rows without an adapter cost their id's read.
+// z goes through the workspace (fp32): launches for it, and one that adds its product
+// to y.  Rows without an adapter cost their id's read.  What bounds it: for prompts the
+// bytes of x and twice those of y, which are far more than the adapters' and whose
+// products take the matrix units a tenth of that time; for few rows the launches.
+// 8192 bf16 rows, K 2560, N 6912, rank 64, nine requests: 120 us (24 + 6 + 90; 495 MB
+// at the 4.8 TB/s of a large copy are 103); 1500 of K 6912, N 2560, rank 32, from the
+// last-level cache: 28 (13 + 4 + 11); 48 rows, K 2560, N 7680, rank 16, each its own
+// adapter: 11; one row 6.
 #include <type_traits>
 
 #include "block_internal.h"
@@ -43,7 +49,8 @@ __device__ __forceinline__ void eight_bf16(const uint4& u, float (&v)[8]) {
 // ---------------------------------------------------------------- few rows
 //
 // fp32 FMA of the vector units; A and B are read with 16 bytes a lane, eight
-// neighbours of K (ranks) each.
+// neighbours of K (ranks) each: a row reads its adapter from an L2 or the last-level
+// cache whatever its neighbours do.
 
 // Sums of V[0 .. n - 1] over the wave's lanes.  Two values change halves with one
 // swap of 32 lanes, then of 16: a lane goes on with a quarter of them; four
@@ -182,22 +189,22 @@ hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
 // Both products on the bf16 MFMA.  fp32 values enter as three exact bf16 planes,
 // smallest first, so products are exact and sums fp32.  A tile of tokens goes
 // through each adapter that occurs in it, whole, and every token keeps the result
-// of its own: no sorting, no zeros multiplied into other rows (an infinity in one
-// adapter stays with its tokens), and a tile costs its number of adapters, which for
-// prompts is one or two.
+// of its own: no zeros multiplied into other rows (an infinity in one adapter stays
+// with its tokens), and a tile costs its number of adapters.  For prompts that is one
+// or two; tokens in any order are first put in the order of their adapters.
 //
 // An MFMA operand wants neighbouring lanes in different rows, memory wants them side
 // by side: four lanes in four rows take four times the address cycles.  So what a
 // work-group shares goes through LDS, and y is read and written an element a lane,
-// 32 side by side.  A tile of more than kFew adapters (a batch of single tokens)
-// goes without LDS: its waves take the adapters of their own tokens one by one,
-// operands straight from memory.  The products and sums of a token are the same,
-// in the same order, either way.
+// 32 side by side.  A tile of more than kFew adapters goes without LDS: its waves
+// take the adapters of their own tokens one by one, operands straight from memory (2048
+// rows of 48 adapters, rank 16: 35 us with kFew 3, 46 with 6, 49 with 12).  The
+// products and sums of a token are the same, in the same order, either way.
 
 constexpr int kTile = 64;    // tokens of a shrink work-group, 16 a wave
 constexpr int kTokens = 128; // tokens of an expand work-group, 32 a wave
 constexpr int kFew = 3;
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = 16;  // what they add to z's bytes would show
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -226,9 +233,11 @@ struct Adapters {
 constexpr uint32_t kNone = 0x80000000u;
 
 // Tokens in any order are put in the order of their adapters, segment by segment, so
-// that a wave meets few of them.  Every work-group of a segment does this for itself.
+// that a wave meets few of them.  Every shrink work-group of a segment does this for
+// itself, 3 us, less than a launch.  1024 fp32 rows of 48 adapters in any order, rank 64,
+// K and N 2560: 41 us, as they come 156; 4096 of 32, rank 32, K and N 2048: 37 and 114.
 constexpr int kSegment = 1024;
-constexpr int kRuns = 32;
+constexpr int kRuns = 32;  // two more adapters a tile, on average
 // key: the place in the segment, and above its ten bits the adapter (a.adapters: none, or
 // past the last row).  False, and nothing written, where ids change at most kRuns times from
 // row to row.  Sorted by one bit of the adapter after the other, stably, four places a thread.
@@ -750,6 +759,8 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
   }
 }
 
+// Two work-groups a CU, each with 128 elements of K at least.  The prompts of the head
+// of this file: 2 splits 23.4 us, 4 (this rule) 23.0, 8 26.7, 16 30.8; fp32 x: 42, 39, 39, 43.
 int splits_for(int64_t rows, int K) {
   const int64_t tiles = (rows + kTile - 1) / kTile;
   const int64_t want = 512 / tiles, most = (K + 127) / 128;
@@ -776,7 +787,8 @@ hipError_t launch_tiles(const AdapterArgs& a, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int groups = (a.rows + kTokens - 1) / kTokens, blocks = (a.N + 63) / 64;
-  int stripes = ((a.R <= 64 ? 1536 : 1024) + groups - 1) / groups;  // with 3 and 2 work-groups a CU
+  // six and four work-groups a CU, of which two and one fit at once
+  int stripes = ((a.R <= 64 ? 1536 : 1024) + groups - 1) / groups;
   if (stripes > blocks) stripes = blocks;
   const int stripe = (blocks + stripes - 1) / stripes * 64;
   stripes = (a.N + stripe - 1) / stripe;
