@@ -83,21 +83,16 @@ __device__ __forceinline__ void sums(float (&v)[N]) {
   }
 }
 
-// A wave forms J ranks of a token's z, 512 elements of K a step.
+// A wave forms J ranks of a token's z, 512 elements of K a step: every `step`-th of them
+// from k0 on.  The sum of rank i of the J is in the lanes 16 i .. 16 i + 15.
 constexpr int J = 4;
 template <int BF>
-__global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m = blockIdx.x;
-  const int j0 = (blockIdx.y * 4 + wave) * J;
-  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
-  if (id < 0) return;
-  const int rank = wave_rank_of(a, id);
-  if (j0 >= rank) return;
+__device__ __forceinline__ float four_ranks(const AdapterArgs& a, int64_t m, int id, int rank, int j0, int k0, int step) {
+  const int lane = threadIdx.x & 63;
   const uint16_t* A = a.A + ((int64_t)id * a.R + j0) * a.K;
   float acc[J] = {};
 #pragma unroll 2
-  for (int k = 8 * lane; k < a.K; k += 512) {
+  for (int k = k0 + 8 * lane; k < a.K; k += step) {
     uint4 w[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) w[j] = *reinterpret_cast<const uint4*>(A + (int64_t)(j0 + j < rank ? j : 0) * a.K + k);
@@ -118,70 +113,149 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
     }
   }
   sums(acc);
-  const int j = j0 + (lane >> 4);
-  if ((lane & 15) == 0 && j < rank) a.z[m * a.R + j] = a.scales[id] * acc[0];
+  return acc[0];
 }
 
 // A wave adds to 64 outputs of a token of y.  C = 2^k >= R / 8 lanes share an output,
 // eight ranks each (one 16-byte read of B), in C passes over the 64; lane l keeps the
 // output of pass l % C.
 template <int C>
-__global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
+struct Outputs {
+  static constexpr int per = 64 / C;
+  uint4 b[C];
+  float* y;
+  float old;
+  int c, have;
+  bool in;
+  __device__ __forceinline__ void load(const AdapterArgs& a, int64_t m, int id, int rank, int n0) {
+    const int lane = threadIdx.x & 63;
+    c = lane % C;
+    const int n_mine = n0 + c * per + lane / C;
+    in = n_mine < a.N;
+    y = a.y + m * a.ldy + n_mine;
+    old = in ? *y : 0.0f;
+    have = max(0, min(8, rank - 8 * c));  // ranks of this lane
+    const uint16_t* B = a.B + ((int64_t)id * a.N) * a.R + 8 * c;
+#pragma unroll
+    for (int p = 0; p < C; ++p) {
+      const int n = n0 + p * per + lane / C;
+      b[p] = n < a.N && have > 0 ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.R) : uint4{0u, 0u, 0u, 0u};
+    }
+  }
+  __device__ __forceinline__ void add(const float (&z)[8]) {  // 0 past the lane's ranks
+    float mine = 0.0f;
+#pragma unroll
+    for (int p = 0; p < C; ++p) {
+      float w[8];
+      eight_bf16(b[p], w);
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v = __builtin_fmaf(z[i], i < have ? w[i] : 0.0f, v);
+      if constexpr (C > 1) v = dpp_add<0xB1>(v);
+      if constexpr (C > 2) v = dpp_add<0x4E>(v);
+      if constexpr (C > 4) v = dpp_add<0x141>(v);
+      if constexpr (C > 8) v = dpp_add<0x140>(v);
+      if (c == p) mine = v;
+    }
+    if (in) *y = old + mine;
+  }
+};
+
+template <int BF>
+__global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m = blockIdx.x;
+  const int j0 = (blockIdx.y * 4 + wave) * J;
+  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
+  if (id < 0) return;
+  const int rank = wave_rank_of(a, id);
+  if (j0 >= rank) return;
+  const float z = four_ranks<BF>(a, m, id, rank, j0, 0, 512);
+  const int j = j0 + (lane >> 4);
+  if ((lane & 15) == 0 && j < rank) a.z[m * a.R + j] = a.scales[id] * z;
+}
+
+template <int C>
+__global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m = blockIdx.x;
   const int n0 = (blockIdx.y * 4 + wave) * 64;
   if (n0 >= a.N) return;
   const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
   if (id < 0) return;
-  const int rank = wave_rank_of(a, id);
-  const int c = lane % C, per = 64 / C;
-  const int n_mine = n0 + c * per + lane / C;
-  float* y = a.y + m * a.ldy;
-  float old = 0.0f;
-  if (n_mine < a.N) old = y[n_mine];
-  const int have = max(0, min(8, rank - 8 * c));  // ranks of this lane
-  const uint16_t* B = a.B + ((int64_t)id * a.N) * a.R + 8 * c;
-  uint4 b[C];
-#pragma unroll
-  for (int p = 0; p < C; ++p) {
-    const int n = n0 + p * per + lane / C;
-    b[p] = n < a.N && have > 0 ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.R) : uint4{0u, 0u, 0u, 0u};
-  }
+  Outputs<C> out;
+  out.load(a, m, id, wave_rank_of(a, id), n0);
   float z[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = i < have ? a.z[m * a.R + 8 * c + i] : 0.0f;
-  float mine = 0.0f;
-#pragma unroll
-  for (int p = 0; p < C; ++p) {
-    float w[8];
-    eight_bf16(b[p], w);
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v = __builtin_fmaf(z[i], i < have ? w[i] : 0.0f, v);
-    if constexpr (C > 1) v = dpp_add<0xB1>(v);
-    if constexpr (C > 2) v = dpp_add<0x4E>(v);
-    if constexpr (C > 4) v = dpp_add<0x141>(v);
-    if constexpr (C > 8) v = dpp_add<0x140>(v);
-    if (c == p) mine = v;
-  }
-  if (n_mine < a.N) y[n_mine] = old + mine;
+  for (int i = 0; i < 8; ++i) z[i] = i < out.have ? a.z[m * a.R + 8 * out.c + i] : 0.0f;
+  out.add(z);
 }
 
-hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
+// Both in one launch: 16 waves form the token's z for themselves, in fours of ranks and
+// parts of K, and add to 1024 outputs, whose y and B are on their way meanwhile.
+constexpr int kWide = 1024;
+constexpr int kTokenMaxRank = 32;
+template <int BF, int C>
+__global__ __launch_bounds__(1024) void token_kernel(AdapterArgs a) {
+  __shared__ float sz[16 * J];  // [part][rank]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m = blockIdx.x;
+  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
+  if (id < 0) return;
+  const int rank = wave_rank_of(a, id);
+  const int n0 = blockIdx.y * kWide + 64 * wave;
+  Outputs<C> out;
+  out.load(a, m, id, rank, n0);
+  const int fours = a.R / J, parts = 16 / fours, part = wave / fours, j0 = (wave - part * fours) * J;
+  if (part < parts && j0 < rank) {
+    const float z = four_ranks<BF>(a, m, id, rank, j0, 512 * part, 512 * parts);
+    if ((lane & 15) == 0) sz[part * a.R + j0 + (lane >> 4)] = z;
+  }
+  __syncthreads();
+  const float s = a.scales[id];
+  float z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v = 0.0f;
+    if (i < out.have) {
+      for (int part = 0; part < parts; ++part) v += sz[part * a.R + 8 * out.c + i];
+    }
+    z[i] = s * v;
+  }
+  if (n0 < a.N) out.add(z);
+}
+
+template <int C>
+hipError_t launch_rows_of(const AdapterArgs& a, hipStream_t s) {
+  // One launch while A is read again for few stripes: alone on the card it takes what two take
+  // (rank 16, K 2560, N 7680: a row 5.2 us and 5.5, 48 rows 7.7 and 7.8, 160 17 and 14), and
+  // the call costs 2.5 us less of the host.  From rank 64 on a work-group has too much of A to
+  // itself (a row 8.3 us and 6.4).
+  if constexpr (8 * C <= kTokenMaxRank) {
+    const int stripes = (a.N + kWide - 1) / kWide;
+    if ((int64_t)a.rows * stripes * a.R * a.K <= 1 << 24) {
+      const dim3 grid(a.rows, stripes);
+      if (a.x_bf16) token_kernel<1, C><<<grid, 1024, 0, s>>>(a);
+      else token_kernel<0, C><<<grid, 1024, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
   const dim3 shrink(a.rows, (a.R + 4 * J - 1) / (4 * J));
   if (a.x_bf16) shrink_rows_kernel<1><<<shrink, 256, 0, s>>>(a);
   else shrink_rows_kernel<0><<<shrink, 256, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 expand(a.rows, (a.N + 255) / 256);
-  const int c = a.R / 8;
-  void (*fn)(AdapterArgs) = c <= 1   ? expand_rows_kernel<1>
-                            : c <= 2 ? expand_rows_kernel<2>
-                            : c <= 4 ? expand_rows_kernel<4>
-                            : c <= 8 ? expand_rows_kernel<8>
-                                     : expand_rows_kernel<16>;
-  fn<<<expand, 256, 0, s>>>(a);
+  expand_rows_kernel<C><<<dim3(a.rows, (a.N + 255) / 256), 256, 0, s>>>(a);
   return hipGetLastError();
+}
+
+hipError_t launch_rows(const AdapterArgs& a, hipStream_t s) {
+  const int c = a.R / 8;
+  return c <= 1   ? launch_rows_of<1>(a, s)
+         : c <= 2 ? launch_rows_of<2>(a, s)
+         : c <= 4 ? launch_rows_of<4>(a, s)
+         : c <= 8 ? launch_rows_of<8>(a, s)
+                  : launch_rows_of<16>(a, s);
 }
 
 // --------------------------------------------------------------- many rows

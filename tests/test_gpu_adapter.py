@@ -66,6 +66,8 @@ SIZES = [  # rows, K, N, adapters, max_rank
     (48, 2560, 512, 32, 16), (64, 136, 129, 7, 128), (65, 384, 192, 4, 64), (100, 6912, 256, 8, 32), (129, 640, 68, 2, 72),
     (500, 2048, 1000, 6, 16), (700, 5632, 130, 3, 48), (1031, 264, 260, 40, 8), (2100, 512, 515, 5, 128), (5000, 96, 64, 3, 16),
     (257, 8, 1, 3, 8), (300, 136, 77, 2, 24), (400, 520, 200, 20, 64), (320, 1032, 130, 9, 128), (600, 2048, 65, 70, 32), (1200, 304, 260, 30, 48),
+    # few rows in one launch (rank up to 32, few outputs) and in two
+    (1, 2560, 1100, 2, 8), (5, 2056, 2050, 3, 32), (70, 1544, 1025, 9, 16), (3, 512, 1024, 2, 24), (9, 6912, 3100, 4, 32), (600, 1032, 1030, 5, 32),
     # in tiles: rows (K + N) of 5 2^19 and more
     (257, 8, 10400, 3, 8), (300, 136, 8800, 2, 24), (400, 6520, 200, 20, 64), (320, 8200, 130, 9, 128), (600, 4360, 65, 70, 32),
     (1200, 304, 1999, 30, 48), (5000, 456, 77, 3, 16), (2100, 1024, 515, 5, 128), (40000, 8, 64, 200, 8), (3000, 640, 257, 1500, 8),
@@ -164,7 +166,7 @@ def test_strides_and_rows_without_an_adapter(lq, rows, K, N, n, R):
     assert (got == 3.5).all()
 
 
-@pytest.mark.parametrize("rows,K,N,n,R", [(9, 1024, 300, 4, 16), (260, 1024, 300, 4, 64), (1300, 640, 100, 8, 16), (700, 2048, 300, 12, 64),
+@pytest.mark.parametrize("rows,K,N,n,R", [(9, 1024, 300, 4, 16), (12, 2560, 2300, 4, 24), (400, 2048, 1500, 4, 16), (260, 1024, 300, 4, 64), (1300, 640, 100, 8, 16), (700, 2048, 300, 12, 64),
                                              (300, 640, 130, 9, 128), (1000, 1024, 68, 40, 24), (1300, 1960, 100, 8, 16), (700, 2048, 1800, 12, 64),
                                              (300, 640, 8130, 9, 128), (1100, 2408, 68, 40, 24)])
 def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
@@ -183,11 +185,11 @@ def test_a_row_does_not_depend_on_other_rows(lq, rows, K, N, n, R):
         assert torch.equal(one[mine], mixed[mine])
 
 
-@pytest.mark.parametrize("rows, dtype, N", [(40, BF16, 68), (300, BF16, 8600), (300, F32, 8600)])
-def test_rows_far_apart(lq, rows, dtype, N):
+@pytest.mark.parametrize("rows, dtype, N, n", [(40, BF16, 68, 3), (300, BF16, 8600, 3), (300, BF16, 8600, 9), (300, F32, 8600, 9)])
+def test_rows_far_apart(lq, rows, dtype, N, n):
     """Row distances at the limit: a tile spans almost 2^31 bytes, the matrix much more."""
     rng = np.random.default_rng(rows)
-    K, n, R, ld = 264, 3, 16, (1 << 24) - 8
+    K, R, ld = 264, 16, (1 << 24) - 8
     ldx = ld if dtype is BF16 else (1 << 23) - 8
     x, A, B, s, y = whole(rng, rows, K, N, n, R)
     ids = rng.integers(-1, n, rows)
