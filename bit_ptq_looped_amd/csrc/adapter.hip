@@ -3,9 +3,10 @@
 //   z_m = scale_a A_a x_m,  y_m += B_a z_m,  a = ids[m].
 //
 // z goes through the workspace (fp32) from the launches that form it to the one that
-// adds its product to y, or stays in one launch (few rows).  Rows without an adapter cost their id's read.  What bounds it: for prompts the
-// bytes of x and twice those of y, which are far more than the adapters' and whose
-// products take the matrix units a tenth of that time; for few rows the launches.
+// adds its product to y, or stays in one launch (few rows).  Rows without an adapter
+// cost their id's read.  What bounds it: for prompts the bytes of x and twice those of
+// y, which are far more than the adapters' and whose products take the matrix units a
+// tenth of that time; for few rows the launch and its trips to memory.
 // 8192 bf16 rows, K 2560, N 6912, rank 64, nine requests: 120 us (24 + 6 + 90; 495 MB
 // at the 4.8 TB/s of a large copy are 103); 1500 of K 6912, N 2560, rank 32, from the
 // last-level cache: 28 (13 + 4 + 11); 48 rows, K 2560, N 7680, rank 16, each its own

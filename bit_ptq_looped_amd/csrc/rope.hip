@@ -10,8 +10,8 @@
 // tensors: the first heads' loads are issued before the position is looked up.
 // 8192 tokens of 32 heads of 128: bf16 28 us, fp32 53 (4.8 and 5.0 TB/s, a large
 // copy reaches 4.8); 16384 tokens of 16 heads each of fp32 queries, keys and values,
-// keys and values into the cache, queries out in bf16:
-// 117 (5.2 TB/s); a single token 3.0, of which all but a fraction is the launch.
+// keys and values into the cache, queries out in bf16: 117 (5.2 TB/s); a single token
+// 3.0, of which all but a fraction is the launch.
 //
 // The row of a token is found by a search of the wave, 64 probes of cu at once:
 // one trip to memory for up to 64 rows, two up to 4096.
