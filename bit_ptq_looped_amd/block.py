@@ -161,8 +161,9 @@ def loopq_kv_write_rope(pool, slab: int, table: KVTable, cu, rope: Rope, k, v, q
     (bfloat16 or float32; q itself if it has that type)."""
     _types()
     p = _pool(pool)
-    kp, ldk = _rows3(k, p.heads, p.head_dim, "k")
-    vp, ldv = _rows3(v, p.heads, p.head_dim, "v")
+    heads, dim = p.heads, p.head_dim
+    kp, ldk = _rows3(k, heads, dim, "k")
+    vp, ldv = _rows3(v, heads, dim, "v")
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must have one type and shape")
     qp = op = None
@@ -170,8 +171,8 @@ def loopq_kv_write_rope(pool, slab: int, table: KVTable, cu, rope: Rope, k, v, q
     if q is not None:
         if q.dtype != k.dtype or q.shape[0] != k.shape[0] or q_out is None or q_out.shape != q.shape:
             raise ValueError("q must have k's type and tokens, q_out its shape")
-        qp, ldq = _rows3(q, None, p.head_dim, "q")
-        op, ldo = _rows3(q_out, None, p.head_dim, "q_out")
+        qp, ldq = _rows3(q, None, dim, "q")
+        op, ldo = _rows3(q_out, None, dim, "q_out")
         heads_q, q_dtype = q.shape[1], _dtype_code(q_out)
     _check(load().loopq_kv_write_rope(_ref(p), slab, _ref(_table(table)), _ints(cu, "cu", table.lens.numel() + 1),
                                       _ref(_rope(rope)), kp, ldk, vp, ldv, _dtype_code(k), k.shape[0], qp, ldq,

@@ -91,7 +91,9 @@ def _types():
 def _ints(t, what: str, n: int = 0) -> int:
     if t.dtype is not (_torch or _types()).int32 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} values")
-    return _ptr(t)
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    return t.data_ptr()
 
 
 def _table(t: KVTable) -> _Table:
@@ -110,7 +112,9 @@ def _rows3(x, heads, dim: int, what: str):
     row, head, one = x.stride()
     if (one != 1 or (head != dim and shape[1] > 1)) and x.numel():
         raise ValueError(f"{what}: heads and elements of a token must be dense")
-    return _ptr(x), (row if shape[0] > 1 else shape[1] * dim)
+    if not x.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    return x.data_ptr(), (row if shape[0] > 1 else shape[1] * dim)
 
 
 def _ws(workspace):
