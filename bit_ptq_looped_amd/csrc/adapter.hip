@@ -11,6 +11,7 @@
 // at the 4.8 TB/s of a large copy are 103); 1500 of K 6912, N 2560, rank 32, from the
 // last-level cache: 28 (13 + 4 + 11); 48 rows, K 2560, N 7680, rank 16, each its own
 // adapter: 8; one row 5.
+#include <algorithm>
 #include <type_traits>
 
 #include "block_internal.h"
@@ -836,9 +837,10 @@ __global__ __launch_bounds__(256, RS <= 4 ? 2 : 1) void expand_tile_kernel(Adapt
 
 // Two work-groups a CU, each with 128 elements of K at least.  The prompts of the head
 // of this file: 2 splits 23.4 us, 4 (this rule) 23.0, 8 26.7, 16 30.8; fp32 x: 42, 39, 39, 43.
+constexpr int kShrinkGroups = 512;
 int splits_for(int64_t rows, int K) {
   const int64_t tiles = (rows + kTile - 1) / kTile;
-  const int64_t want = 512 / tiles, most = (K + 127) / 128;
+  const int64_t want = kShrinkGroups / tiles, most = (K + 127) / 128;
   const int64_t n = want < most ? want : most;
   return (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
@@ -877,9 +879,12 @@ hipError_t launch_tiles(const AdapterArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// z of each split of K (at most what splits_for gives for any K), its planes, the order
+// z of each split of K, its planes, the order.  splits_for falls in steps as rows grow, so
+// splits times rows goes up and down: room is taken for the most that it reaches for any
+// number of rows up to this one and any K, and what serves a batch serves every smaller one.
 static size_t sums_bytes(int64_t rows, int max_rank) {
-  return (size_t)(splits_for(rows > 0 ? rows : 1, 1 << 30) * rows * max_rank * 4 + 255) / 256 * 256;
+  const int64_t split = std::min<int64_t>(kMaxSplits * rows, kShrinkGroups * kTile);
+  return (size_t)(std::max(rows, split) * max_rank * 4 + 255) / 256 * 256;
 }
 static size_t planes_bytes(int64_t rows, int max_rank) { return (size_t)(rows * max_rank * 6 + 255) / 256 * 256; }
 size_t adapter_workspace_bytes(int64_t rows, int max_rank) {

@@ -134,8 +134,9 @@ int32_t loopq_kv_write_rope(const loopq_kv_pool* pool_host, int32_t slab, const 
  * end as NaN).
  * max_rank a multiple of 8 up to 128; K % 8 == 0, K <= 65536; N <= 2^20;
  * adapters <= 2^16; rows <= 2^20; ldx < 2^24 (fp32: 2^23),
- * ldy < 2^24.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank);
- * two calls that share one must not overlap. */
+ * ldy < 2^24.  Workspace: loopq_adapter_workspace_bytes(rows, max_rank), which
+ * never falls as either grows: one of a program's largest batch and rank serves all
+ * of its calls.  Two calls that share one must not overlap. */
 int32_t loopq_adapter_workspace_bytes(int32_t rows, int32_t max_rank, size_t* bytes_host);
 int32_t loopq_adapter_apply(const void* x, int64_t ldx, int32_t dtype, int32_t rows, int32_t K, int32_t N,
                             const int32_t* ids, const void* A, const void* B, const float* scales,

@@ -222,3 +222,18 @@ def test_adapter_workspace(lib):
         with pytest.raises(loopq.LoopQError) as e:
             block.loopq_adapter_workspace_bytes(*args)
         assert e.value.status == want
+
+
+def test_an_adapter_workspace_serves_smaller_calls(lib):
+    """A server allocates once, for its largest batch and rank: no call of fewer rows or of a smaller rank needs more."""
+    counts = list(range(0, 2600)) + [n + d for n in range(2624, 70000, 64) for d in (-1, 0, 1)] + [131072, 1 << 20]
+    for rank in (8, 64, 128):
+        need = [block.loopq_adapter_workspace_bytes(n, rank) for n in counts]
+        assert need == sorted(need)
+    for n in (1, 65, 2048, 2112, 40000):
+        need = [block.loopq_adapter_workspace_bytes(n, r) for r in range(8, 129, 8)]
+        assert need == sorted(need)
+    # the call asks for no more than that: a workspace of enough bytes is only refused for its alignment
+    for most, rows in ((17000, 8192), (17000, 16384), (2112, 2048), (8256, 8192), (1 << 20, 32768)):
+        size = block.loopq_adapter_workspace_bytes(most, 64)
+        assert adapter(lib, rows=rows, K=8, ldx=8, N=1, ldy=1, max_rank=64, ws=FAKE + 7 * MB + 64, size=size) == ALIGNMENT

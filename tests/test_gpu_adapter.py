@@ -242,3 +242,18 @@ def test_on_a_stream_and_in_a_graph(lq, rows):
         torch.cuda.synchronize()
         assert torch.equal(y, want)
         step()
+
+
+def test_one_workspace_serves_every_call(lq):
+    """The workspace of a program's largest batch and rank, with what other calls left in it."""
+    rng = np.random.default_rng(5)
+    K, N, n = 512, 320, 4
+    ws = block.empty_adapter_workspace(8256, 64)
+    ws.view(torch.float32).fill_(float("nan"))
+    for rows, R in ((8256, 64), (8192, 64), (5, 16), (2048, 64), (300, 32), (8192, 8)):
+        x, A, B = dev(rng.standard_normal((rows, K))), dev(rng.standard_normal((n, R, K)), BF16), dev(rng.standard_normal((n, N, R)), BF16)
+        s, y, ids = dev(rng.uniform(-2, 2, n), F32), dev(rng.standard_normal((rows, N))), np.sort(rng.integers(-1, n, rows))
+        want = y.clone()
+        apply(x, ids, A, B, s, want)
+        block.loopq_adapter_apply(x, i32(ids), A, B, s, y, ws)
+        assert torch.equal(y, want)
