@@ -6,10 +6,14 @@
 // the load to the last store, so each input is read once and each output
 // written once: the kernel is bound by those bytes.
 //
-// The mean is taken in 64 bits: a square of an fp32 number is exact there (48
-// bits) and the sum of 2^15 of them carries an error below 2^-37 of an fp32
-// ulp's half, so r is one fp32 number whatever the order of summation, and with
-// it the codes, which are compared bit for bit like every code of this library.
+// The mean is taken in 64 bits: a square of an fp32 number is exact there (48 bits), the
+// sum of a row's squares is rounded at most 52 times on the way of any of them (4 NC - 1 in
+// a thread, 6 between lanes, 15 between waves, in the longest form), and 1 / K, the
+// product with it and eps take a rounding each: 55 2^-53, of which the root takes half.
+// With the root's own 2^-52 the value that becomes r is within 2^-48 of itself.  So r is one
+// fp32 number whatever the order of summation, but for a row whose exact value lies that
+// close to the border between two of them (less than one in 2^23), and with it the codes,
+// which are compared bit for bit like every code of this library.
 // It costs one conversion and one fp64 FMA an element, in a kernel that waits for
 // memory: 8192 rows of 2560, fp32 with an fp32 residual into sums and 8-bit codes, take
 // 50 us (275 MB, 5.5 TB/s; a large copy reaches 4.8), bf16 to bf16 19, 4096 of 6912 bf16
@@ -141,13 +145,15 @@ __device__ __forceinline__ float row_max(float v, float* part) {
   return v;
 }
 
-// fl32(1 / sqrt(mean + eps)): the hardware's reciprocal root (at least 24 bits)
-// and one Newton step, whose error, 3/2 of the square, stays below 2^-46.
+// fl32(1 / sqrt(mean + eps)).  The hardware's reciprocal root y carries some 24 bits; with
+// e = 1 - v y^2 the root is y (1 - e)^(-1/2) = y (1 + e / 2 + 3 e^2 / 8 + ..), and what is left
+// out, 5 e^3 / 16, lies below 2^-65: e is off by the rounding of v y, at most 2^-53, which
+// halves, and the last FMA rounds once more.  Below 2^-52 together.
 __device__ __forceinline__ float reciprocal_root(double mean, double eps) {
   const double v = mean + eps;
   const double y = __builtin_amdgcn_rsq(v);
-  const double e = __builtin_fma(-v * y, y, 1.0);  // 1 - v y^2
-  const float r = (float)__builtin_fma(0.5 * e, y, y);
+  const double e = __builtin_fma(-v * y, y, 1.0);
+  const float r = (float)__builtin_fma(y * e, __builtin_fma(0.375, e, 0.5), y);
   return v < __builtin_huge_val() ? r : (float)y;  // infinite: 0, NaN: NaN
 }
 

@@ -39,9 +39,10 @@ extern "C" {
  * (per_token 1) without a transform forms them from z: bitwise the same, ready
  * for loopq_gemm_codes.  clip > 0 and finite, bits_a 4 or 8 (both ignored without
  * codes).
- * In 64 bits the order of the sum does not show in r (but where the exact value
- * lies within some 2^-50 of a border between two fp32 numbers), so y, codes and
- * steps are functions of the inputs, not of the launch.
+ * What 64 bits round stays below 2^-48 of r before it is rounded to fp32.  So the
+ * order of the sum does not show in r, and y, codes and steps are functions of the
+ * inputs, not of the launch, but for a row whose exact 1 / sqrt lies within 2^-48 of
+ * itself of the border between two fp32 numbers (less than one row in 2^23).
  * A row that holds an infinity or NaN (after the rounding of h) has steps of NaN
  * and codes of 0; its y is what the formulas give.
  *

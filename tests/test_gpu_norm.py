@@ -250,3 +250,47 @@ def test_on_a_stream_and_in_a_graph(lq):
         torch.cuda.synchronize()
         assert all(torch.equal(got[k], want[k]) for k in want)
         run(x, res, w, torch.bfloat16)
+
+
+def far_from_a_border(n, seed, lo, hi):
+    """x [n][8] whose r lies 2^-hi .. 2^-lo of itself above or below the border between two fp32 numbers; the nearer one of each.
+
+    Four elements are chosen one after the other, each the largest fp32 number whose square does not exceed what is
+    left of the sum; the last is 2^-20, so that y there is r 2^-20, exactly."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 70
+    rng = np.random.default_rng(seed)
+    x, r = np.zeros((n, 8), dtype=np.float32), np.zeros(n, dtype=np.float32)
+    eps = Decimal(float(EPS))
+    for m in range(n):
+        below = np.float32(rng.uniform(0.25, 4.0))
+        above = np.nextafter(below, np.float32(8))
+        border = (Decimal(float(below)) + Decimal(float(above))) / 2
+        off = Decimal(float(rng.choice([-1, 1]) * 2.0 ** -rng.uniform(lo, hi)))
+        left = (1 / (border * (1 + off)) ** 2 - eps) * 8 - Decimal(2) ** -40
+        x[m, 7] = 2.0 ** -20
+        for i in range(4):
+            h = np.float32(float(left.sqrt()))
+            while Decimal(float(h)) ** 2 > left:
+                h = np.nextafter(h, np.float32(0))
+            x[m, i] = h
+            left -= Decimal(float(h)) ** 2
+        mean = sum(Decimal(float(v)) ** 2 for v in x[m]) / 8
+        true = 1 / (mean + eps).sqrt()
+        assert Decimal(2) ** Decimal(-hi - 0.1) < abs(true / border - 1) < Decimal(2) ** Decimal(-lo + 0.1)
+        r[m] = above if true > border else below
+    return x, r
+
+
+def test_the_root_has_its_64_bits(lq):
+    """Rows whose r lies close to a border between two fp32 numbers, farther from it than the roundings of 64 bits reach.
+
+    Of eight elements five are not zero: the sum is rounded four times, the mean (an eighth of it) never, eps is added
+    with one rounding, and a root takes half of an error on: 2.5 2^-53 before the root, which adds less than 2^-52.
+    Together below 2^-51; the rows stay 2^-50 away."""
+    x, want = far_from_a_border(3000, 31, 46.0, 49.8)
+    y = torch.empty((3000, 8), device="cuda")
+    block.loopq_rms_norm(torch.from_numpy(x).cuda(), None, float(EPS), y=y)
+    got = y[:, 7].cpu().numpy() * np.float32(2.0 ** 20)
+    wrong = got != want
+    assert not wrong.any(), f"{int(wrong.sum())} of {len(want)} rows"
