@@ -294,3 +294,96 @@ def test_the_root_has_its_64_bits(lq):
     got = y[:, 7].cpu().numpy() * np.float32(2.0 ** 20)
     wrong = got != want
     assert not wrong.any(), f"{int(wrong.sum())} of {len(want)} rows"
+
+
+# ---------------------------------------------- work-groups that take several rows
+
+# widths, and the threads that a row of them gets where there are many rows
+TURNS = [(96, 32), (480, 64), (1024, 128), (1056, 256), (2560, 256), (4096, 256), (6912, 256), (8192, 512)]
+
+
+def turns(T):
+    """Rows of one turn of the launch (8192 threads a CU), and so many that every work-group takes two and some a third."""
+    once = torch.cuda.get_device_properties(0).multi_processor_count * 8192 // T
+    return once, 2 * once + once // 3 + 5
+
+
+def same(a, b):
+    return all(torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)) for k in a)
+
+
+def turned(once, call, out):
+    """The same call a turn's rows at a time, into other buffers."""
+    other = {k: torch.zeros_like(v) for k, v in out.items()}
+    rows = next(iter(out.values())).shape[0]
+    for at in range(0, rows, once):
+        part = slice(max(0, min(at, rows - once)), at + once)
+        call(part, {k: v[part] for k, v in other.items()})
+    return other
+
+
+def pick(rows, once, bad):
+    """Rows to compare with the host: both sides of each turn's end, and some between."""
+    some = set(np.random.default_rng(rows).integers(0, rows, 24).tolist())
+    for at in (0, once, 2 * once, rows):
+        some |= {at + d for d in (-2, -1, 0, 1)}
+    return sorted(r for r in some if 0 <= r < rows and r not in bad)
+
+
+@pytest.mark.parametrize("K,T", TURNS)
+def test_rows_of_several_turns(lq, K, T):
+    """Codes and numbers, the sum over the residual: as with one row a work-group, and as on the host."""
+    once, rows = turns(T)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x, res = torch.randn((rows, K), generator=g, device="cuda"), (3 * torch.randn((rows, K), generator=g, device="cuda")).bfloat16()
+    w = 1 + 0.2 * torch.randn(K, generator=g, device="cuda")
+    bad = {1: float("nan"), once + 1: float("inf"), 2 * once + 1: float("-inf"), rows - 3: float("nan")}
+    for r, v in bad.items():
+        x[r, (7 * r) % K] = v
+    out = dict(y=torch.empty((rows, K), dtype=torch.bfloat16, device="cuda"), sum_out=torch.empty_like(res),
+               codes=torch.empty((rows, K), dtype=torch.int8, device="cuda"), steps=torch.empty((rows, K // 32), device="cuda"))
+    block.loopq_rms_norm(x, w, float(EPS), residual=res, bits_a=4, clip=0.75, **out)
+    assert same(out, turned(once, lambda p, o: block.loopq_rms_norm(x[p], w, float(EPS), residual=res[p], bits_a=4, clip=0.75, **o), out))
+    at = pick(rows, once, bad)
+    check(x[at], res[at], w, {k: v[at] for k, v in out.items()}, bits=4, clip=0.75)
+    for r in bad:
+        assert out["steps"][r].isnan().all() and not out["codes"][r].any()
+    # in place: the sum over the residual, the codes as before
+    again = dict(out, y=None, sum_out=res, codes=torch.zeros_like(out["codes"]), steps=torch.zeros_like(out["steps"]))
+    block.loopq_rms_norm(x, w, float(EPS), residual=res, bits_a=4, clip=0.75, **again)
+    assert same({k: out[k] for k in ("sum_out", "codes", "steps")}, {k: again[k] for k in ("sum_out", "codes", "steps")})
+
+
+@pytest.mark.parametrize("K,T", TURNS)
+def test_rows_of_several_turns_with_one_step_a_token(lq, K, T):
+    """bf16 rows over themselves, one step a row: the maximum's exchange between waves as well."""
+    once, rows = turns(T)
+    g = torch.Generator(device="cuda").manual_seed(K + 1)
+    x = torch.randn((rows, K), generator=g, device="cuda").bfloat16()
+    x *= torch.exp(torch.randn((rows, 1), generator=g, device="cuda")).bfloat16()
+    x[torch.arange(rows, device="cuda"), torch.randint(0, K, (rows,), generator=g, device="cuda")] *= 8  # the maximum lies anywhere
+    w = 1 + 0.2 * torch.randn(K, generator=g, device="cuda")
+    bad = {0: float("inf"), once + 2: float("nan"), rows - 1: float("nan")}
+    for r, v in bad.items():
+        x[r, (11 * r) % K] = v
+    out = dict(y=x.clone(), codes=torch.empty((rows, K), dtype=torch.int8, device="cuda"), steps=torch.empty((rows, K // 32), device="cuda"))
+    block.loopq_rms_norm(out["y"], w, float(EPS), bits_a=8, per_token=True, **out)
+    assert same(out, turned(once, lambda p, o: block.loopq_rms_norm(x[p], w, float(EPS), bits_a=8, per_token=True, **o), out))
+    at = pick(rows, once, bad)
+    check(x[at], None, w, dict({k: v[at] for k, v in out.items()}, sum_out=None), bits=8, per_token=True)
+    for r in bad:
+        assert out["steps"][r].isnan().all() and not out["codes"][r].any()
+
+
+@pytest.mark.parametrize("rows,K", [(5, 64), (5, 2048), (700, 2560), (3, 6912), (2, 10560), (2, 32768)])
+def test_token_codes_of_weights_that_are_not_finite(lq, rows, K):
+    """One step a token from z with infinities and NaN: as loopq_quant_act_per_token has it from z."""
+    x = make(rows, K, torch.float32, 28)
+    for bad in ((3.0e38,), (float("nan"),), (float("inf"), float("nan")), (float("-inf"), 3.4e38)):
+        w = torch.ones(K, device="cuda")
+        for i, v in enumerate(bad):
+            w[(13 * i + 3) % K] = v
+        out = run(x, None, w, torch.float32, codes=True, bits_a=8, per_token=True)
+        codes, steps = torch.empty_like(out["codes"]), torch.empty_like(out["steps"])
+        lq.loopq_quant_act_per_token(out["y"], None, None, 1.0, 8, codes, steps)
+        assert torch.equal(codes, out["codes"]) and np.array_equal(f32(steps), f32(out["steps"]), equal_nan=True)
