@@ -303,3 +303,39 @@ def test_on_a_stream_and_in_a_graph(lq):
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(pool.view(torch.int16), want_pool.view(torch.int16))
         step()
+
+
+# ------------------------------------------------ waves that take their heads in several passes
+
+MANY = [(64, 64), (64, 38), (96, 96), (96, 94), (128, 128), (128, 126)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", [HALF, PAIRS])
+@pytest.mark.parametrize("dim,rot", MANY)
+def test_many_heads_of_many_tokens(lq, dim, rot, layout, dtype):
+    """From 4096 tokens on a wave has all 23 heads of its token: two passes and more, the last not full."""
+    tokens, heads = 4100, 23
+    x, f = make((tokens, heads, dim), dtype, dim + rot), freqs(rot)
+    pos = np.random.default_rng(rot).integers(0, 1 << 20, tokens)
+    out = torch.full_like(x, 7.0)
+    block.loopq_rope(x, i32(pos), spec(f, layout, 1.25), out)
+    few = torch.full_like(x, 7.0)  # a hundred tokens at a time: a wave has one pass
+    for at in range(0, tokens, 100):
+        block.loopq_rope(x[at:at + 100], i32(pos[at:at + 100]), spec(f, layout, 1.25), few[at:at + 100])
+    assert torch.equal(out, few)
+    some = np.r_[0:40, 2000:2040, tokens - 40:tokens]
+    want, err = turn(x[some].double().cpu().numpy(), pos[some], f, layout, 1.25)
+    close(out[some], want, err)
+    block.loopq_rope(x, i32(pos), spec(f, layout, 1.25), x)
+    assert torch.equal(x, out)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", [HALF, PAIRS])
+@pytest.mark.parametrize("dim,rot", MANY)
+def test_write_of_many_tokens(lq, dim, rot, layout, dtype):
+    """A wave goes from queries to keys to values, in the middle of a pass as well: 20 + 5 + 5 heads."""
+    rng = np.random.default_rng(dim + rot)
+    check_write(rng, 4, 5, 4, dim, rot, 32, dtype, layout, news=[1500, 0, 1300, 1400], width=80)
+    check_write(rng, 3, 3, 1, dim, rot, 16, dtype, layout, q_dtype=BF16, news=[4100, 1, 7], width=300)
