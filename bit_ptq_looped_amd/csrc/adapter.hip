@@ -7,10 +7,10 @@
 // cost their id's read.  What bounds it: for prompts the bytes of x and twice those of
 // y, which are far more than the adapters' and whose products take the matrix units a
 // tenth of that time; for few rows the launch and its trips to memory.
-// 8192 bf16 rows, K 2560, N 6912, rank 64, nine requests: 120 us (24 + 6 + 90; 495 MB
-// at the 4.8 TB/s of a large copy are 103); 1500 of K 6912, N 2560, rank 32, from the
-// last-level cache: 28 (13 + 4 + 11); 48 rows, K 2560, N 7680, rank 16, each its own
-// adapter: 8; one row 5.
+// 8192 bf16 rows of nine requests, one without an adapter, K 2560, N 6912, rank 64: 120 us
+// (24 + 6 + 90; 458 MB at the 4.8 TB/s of a large copy are 95); 1500 of K 6912, N 2560, rank
+// 32, from the last-level cache: 28 (13 + 4 + 11); 48 rows of 32 adapters, K 2560, N 7680,
+// rank 16: 7.7; one such row 5.2.
 #include <algorithm>
 #include <type_traits>
 
@@ -899,9 +899,13 @@ hipError_t launch_adapter(AdapterArgs a, hipStream_t s) {
   const int64_t most = (int64_t)1 << 31, item = a.x_bf16 ? 2 : 4;
   a.sort = (kSegment - 1) * a.ldx * item + a.K * item < most && (kSegment - 1) * a.ldy * 4 + (int64_t)a.N * 4 < most;
   // Few rows go one by one: tiles cost 14 us (in any order 20 and more) before they do
-  // anything, rows what they read.  rank 16, K and N of 2560, one by one and in tiles:
-  // 400 rows of 4 adapters 12 and 16 us, 600 of 32 in any order 17 and 24; rank 64, N of
-  // 6912: 160 rows 21 and 24, 256 29 and 18, 400 of 32 in any order 48 and 50.
+  // anything, rows what they read.  The rule leaves out the rank and the order of the ids, so
+  // near the border it takes the slower form in places.  One by one and in tiles, of 4 adapters
+  // (the rule's choice starred), K of 2560: rank 16, N of 2560: 256 rows *9 and 14 us, 400 *12
+  // and 16, 600 16 and *17, those in any order 16 and *25; N of 6912: 256 rows *16 and 15;
+  // rank 64, N of 2560: 400 rows *22 and 21, 600 in any order 30 and *35; N of 6912: 256 rows
+  // *29 and 18.  Over 60 sizes around the border (96 to 600 rows, ranks 16 and 64) it takes 5%
+  // more time than the better form on average, 65% at worst.
   return (int64_t)a.rows * (a.K + a.N) <= 5 << 19 ? launch_rows(a, s) : launch_tiles(a, s);
 }
 

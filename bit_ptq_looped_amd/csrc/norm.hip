@@ -4,7 +4,9 @@
 // h = x + residual; r = fl32(1 / sqrt(mean h^2 + eps)); z = (h r) w; out: h, z,
 // or the Eq.(4) codes and steps of z.  A row's elements stay in registers from
 // the load to the last store, so each input is read once and each output
-// written once: the kernel is bound by those bytes.
+// written once: the kernel is bound by those bytes, but where bf16 rows without a
+// residual become codes.  There some 26 vector instructions an element (the squares in 64
+// bits, the quotients and their check, packing) take 87% of the launch's cycles.
 //
 // The mean is taken in 64 bits: a square of an fp32 number is exact there (48 bits), the
 // sum of a row's squares is rounded at most 52 times on the way of any of them (4 NC - 1 in
@@ -17,15 +19,16 @@
 // It costs one conversion and one fp64 FMA an element, in a kernel that waits for
 // memory: 8192 rows of 2560, fp32 with an fp32 residual into sums and 8-bit codes, take
 // 50 us (275 MB, 5.5 TB/s; a large copy reaches 4.8), bf16 to bf16 19, 4096 of 6912 bf16
-// with one step a token 27; one row of 2048 2.2, of which most is the launch.
+// with one step a token 26; one row of 2048 2.5, of which most is the launch.
 #include "block_internal.h"
 #include "quant_core.h"
 
 namespace loopq {
 namespace {
 
-// Threads a CU is given, at most: four times what it holds, so that a work-group
-// has a few rows where there are many and the last ones end together.  8192 rows
+// Threads a CU is given, at most: a CU holds 512 to 2048 by the form's registers (1280 as
+// <256, 3>, 1024 as <256, 7> of bf16), so four to sixteen times that, and a work-group takes
+// a few rows where there are very many while the last ones end together.  8192 rows
 // of 2560, fp32 with an fp32 residual: 2048 threads 54 us, 8192 50; bf16 18.2 and 18.5.
 constexpr int kNormThreads = 8192;
 
@@ -293,7 +296,8 @@ hipError_t launch_form(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
-  // Two to seven runs a thread.  With fewer, a wave's own work (the root, the exchange
+  // Two to seven runs a thread, but one for the shortest rows and for few rows, and eight
+  // for the longest.  With fewer, a wave's own work (the root, the exchange
   // between lanes, its start) shows: 8192 bf16 rows of 2560 take 18.2 us as <256, 3> and
   // 20.4 as <512, 2>, 4096 of 6912 with one step a token 27 as <256, 7>, 31 as <512, 4>.
   // With more, too few waves fit a CU: the 8192 rows take 20.8 us as <64, 10>.

@@ -276,7 +276,7 @@ hipError_t launch_rope(RopeArgs a, hipStream_t s) {
   const int step = 64 / (a.head_dim / (vec ? 16 : 8));  // heads of a pass
   const int passes = (a.heads + step - 1) / step;
   // a token's heads are shared out among waves while there are few tokens: 4096 waves are
-  // four a SIMD, and eight find room
+  // four a SIMD, which is what finds room (five in bf16) by rope_vec_kernel's registers
   const int want = (int)((4096 + (int64_t)a.tokens - 1) / a.tokens);
   int split = want < passes ? want : passes;
   a.per = (passes + split - 1) / split * step;

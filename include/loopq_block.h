@@ -25,7 +25,7 @@ extern "C" {
 
 /* Residual, RMS norm and what the next linear takes, in one pass over the rows.
  *
- *   h = x + residual, rounded to the residual's type (h = x without a residual)
+ *   h = fl32(x + residual), rounded to the residual's type (h = x without a residual)
  *   r = fl32(1 / sqrt(mean_k h_k^2 + eps)), the mean, root and quotient in fp64
  *   z_k = fl32(fl32(h_k r) w_k)        (fl32(h_k r) without a weight)
  *
