@@ -257,3 +257,29 @@ def test_one_workspace_serves_every_call(lq):
         apply(x, ids, A, B, s, want)
         block.loopq_adapter_apply(x, i32(ids), A, B, s, y, ws)
         assert torch.equal(y, want)
+
+
+def by_adapter(x, ids, A, B, s, y):
+    """As reference, an adapter's rows at a time (whole numbers: exact whatever the order)."""
+    out = y.astype(np.float64)
+    order = np.argsort(ids, kind="stable")
+    for part in np.split(order, np.flatnonzero(np.diff(ids[order])) + 1):
+        a = int(ids[part[0]])
+        if 0 <= a < A.shape[0]:
+            out[part] += s[a] * ((x[part].astype(np.float64) @ A[a].T.astype(np.float64)) @ B[a].T.astype(np.float64))
+    return out
+
+
+@pytest.mark.parametrize("rows,K,N,n,R,dtype", [
+    (1 << 20, 8, 3, 5, 8, F32), ((1 << 20) - 1, 8, 2, 5, 8, BF16),  # the most rows
+    (40000, 8, 64, 1 << 16, 8, F32), (300, 8, 64, 1 << 16, 8, BF16),  # the most adapters
+    (3, 8, 1 << 20, 2, 8, F32), (2, 8, 1 << 20, 2, 24, F32),  # the most outputs
+    (45, 65536, 40, 2, 128, F32), (45, 65536, 40, 2, 128, BF16), (30, 65536, 40, 2, 128, F32), (2, 65536, 40, 2, 32, F32)])  # the longest rows
+def test_the_largest_sizes(lq, rows, K, N, n, R, dtype):
+    rng = np.random.default_rng(rows + K + N + n)
+    x, A, B = (rng.integers(-1, 2, size).astype(np.int8) for size in ((rows, K), (n, R, K), (n, N, R)))
+    s, y, ids = rng.choice([0.5, 1.0, 2.0], n), rng.integers(-1000, 1001, (rows, N)), rng.integers(-1, n + 1, rows)
+    ids[:2] = [n - 1, 0]
+    got = dev(y)
+    apply(dev(x, dtype), ids, dev(A, BF16), dev(B, BF16), dev(s, F32), got)
+    assert torch.equal(got.double().cpu(), torch.from_numpy(by_adapter(x, ids, A, B, s, y)))

@@ -339,3 +339,25 @@ def test_write_of_many_tokens(lq, dim, rot, layout, dtype):
     rng = np.random.default_rng(dim + rot)
     check_write(rng, 4, 5, 4, dim, rot, 32, dtype, layout, news=[1500, 0, 1300, 1400], width=80)
     check_write(rng, 3, 3, 1, dim, rot, 16, dtype, layout, q_dtype=BF16, news=[4100, 1, 7], width=300)
+
+
+@pytest.mark.parametrize("rot", [128, 70])
+def test_write_past_32_bits(lq, rot):
+    """Pages whose elements lie more than 2^32 from the pool's start: the same as in a small pool."""
+    heads, dim, page, slabs, rows = 8, 128, 256, 4, 3
+    pages = (1 << 32) // (slabs * 2 * heads * page * dim) + 40
+    news = [700, 1, 300]
+    cu = i32(np.concatenate([[0], np.cumsum(news)]).tolist())
+    k, v, q = (make((sum(news), h, dim), F32, rot + h) for h in (heads, heads, 2 * heads))
+    pools, outs = [], []
+    for n, first in ((12, 0), (pages, pages - 12)):
+        pool = torch.zeros((n, slabs, 2, heads, page, dim), dtype=BF16, device="cuda")
+        table = torch.arange(first, first + 12, dtype=torch.int32, device="cuda").view(3, 4)
+        t = kv.KVTable(table, i32([900, 260, 300]), torch.ones(n, dtype=torch.int32, device="cuda"))
+        out = torch.zeros((sum(news), 2 * heads, dim), dtype=BF16, device="cuda")
+        block.loopq_kv_write_rope(pool, 3, t, cu, spec(freqs(rot)), k, v, q, out)
+        pools.append(pool)
+        outs.append(out)
+    assert torch.equal(pools[0], pools[1][-12:]) and torch.equal(outs[0], outs[1])
+    assert pools[0].any() and not any(pools[1][at:at + 64].any() for at in range(0, pages - 12 - 64, 64))
+    assert not pools[1][-76:-12].any()
