@@ -283,3 +283,28 @@ def test_the_largest_sizes(lq, rows, K, N, n, R, dtype):
     got = dev(y)
     apply(dev(x, dtype), ids, dev(A, BF16), dev(B, BF16), dev(s, F32), got)
     assert torch.equal(got.double().cpu(), torch.from_numpy(by_adapter(x, ids, A, B, s, y)))
+
+
+@pytest.mark.parametrize("rows,N,R", [(40, 260, 16), (40, 260, 64), (300, 8600, 16), (2700, 260, 32)])
+def test_replays_follow_the_ids(lq, rows, N, R):
+    """A captured call, replayed with other ids, ranks and scales in place: in requests, in any order, none at all."""
+    rng = np.random.default_rng(rows + R)
+    K, n = 768, 9
+    x, A, B = dev(rng.standard_normal((rows, K))), dev(rng.standard_normal((n, R, K)), BF16), dev(rng.standard_normal((n, N, R)), BF16)
+    s, ids, ranks, first = dev(np.ones(n)), i32([-1] * rows), i32([0] * n), dev(rng.standard_normal((rows, N)))
+    y, want, ws, other = first.clone(), first.clone(), block.empty_adapter_workspace(rows, R), block.empty_adapter_workspace(rows, R)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block.loopq_adapter_apply(x, ids, A, B, s, y, ws, ranks=ranks)
+    for turn in range(5):
+        now = rng.integers(-1, n + 1, rows)
+        ids.copy_(i32(now if turn % 2 else np.sort(now) if turn < 4 else np.full(rows, -1)))
+        ranks.copy_(i32(rng.integers(-1, R + 2, n)))
+        s.copy_(dev(rng.uniform(-2, 2, n)))
+        y.copy_(first)
+        want.copy_(first)
+        other.view(torch.float32).fill_(float("nan"))
+        block.loopq_adapter_apply(x, ids, A, B, s, want, other, ranks=ranks)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and (turn == 4) == torch.equal(y, first)

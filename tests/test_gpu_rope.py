@@ -361,3 +361,51 @@ def test_write_past_32_bits(lq, rot):
     assert torch.equal(pools[0], pools[1][-12:]) and torch.equal(outs[0], outs[1])
     assert pools[0].any() and not any(pools[1][at:at + 64].any() for at in range(0, pages - 12 - 64, 64))
     assert not pools[1][-76:-12].any()
+
+
+@pytest.mark.parametrize("layout", [HALF, PAIRS])
+@pytest.mark.parametrize("rot", [64, 54])
+def test_what_is_not_turned_keeps_every_bit(lq, rot, layout):
+    """Every bf16 there is as a value and in the part of a head that is not turned: the same bits (a NaN: a NaN), subnormal numbers among them."""
+    bits = torch.arange(-32768, 32768, dtype=torch.int32, device="cuda").to(torch.int16)
+    tokens, heads, dim, page = 256, 4, 128, 32
+    t = kv.KVTable(torch.arange(8, dtype=torch.int32, device="cuda")[None], i32([tokens]), torch.ones(8, dtype=torch.int32, device="cuda"))
+    v = bits.repeat(2).view(BF16).view(tokens, heads, dim)  # 131072 places, 65536 patterns
+    k = v.clone()
+    k[..., :rot] = make((tokens, heads, rot), BF16, rot)
+    pool = torch.zeros((8, 1, 2, heads, page, dim), dtype=BF16, device="cuda")
+    q = torch.zeros_like(k)
+    block.loopq_kv_write_rope(pool, 0, t, i32([0, tokens]), spec(freqs(rot), layout), k, v, k, q)
+    alone = torch.zeros_like(k)
+    block.loopq_rope(k, torch.arange(tokens, dtype=torch.int32, device="cuda"), spec(freqs(rot), layout), alone)
+
+    def kept(got, want):
+        nan = want.isnan()
+        assert torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan]) and got[nan].isnan().all()
+
+    def rows(at):  # [tokens][heads][dim] of the slab's keys or values
+        return pool[:, 0, at].transpose(1, 2).reshape(tokens, heads, dim)
+    kept(rows(1).contiguous(), v)
+    for got in (rows(0), q, alone):
+        kept(got[..., rot:].contiguous(), k[..., rot:].contiguous())
+
+
+def test_replays_follow_what_the_table_holds(lq):
+    """A captured write of a batch's next tokens, replayed as the rows grow."""
+    rng = np.random.default_rng(11)
+    rows, heads, dim, page = 5, 2, 64, 16
+    pool = torch.zeros((60, 1, 2, heads, page, dim), dtype=BF16, device="cuda")
+    table = torch.from_numpy(rng.permutation(60).astype(np.int32)[:50].reshape(5, 10)).cuda()
+    t, cu, f = kv.KVTable(table, i32([0] * 5), torch.ones(60, dtype=torch.int32, device="cuda")), i32(range(6)), spec(freqs(64))
+    q, k, v = (make((rows, h, dim), F32, 40 + i) for i, h in enumerate((4, heads, heads)))
+    out, want = torch.zeros_like(q), torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block.loopq_kv_write_rope(pool, 0, t, cu, f, k, v, q, out)
+    for n in ([1, 16, 17, 2, 160], [2, 17, 18, 100, 33], [3, 18, 161, 0, 34]):
+        t.lens.copy_(i32(n))
+        before = pool.clone()
+        block.loopq_kv_write_rope(before, 0, t, cu, f, k, v, q, want)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(pool.view(torch.int16), before.view(torch.int16)) and torch.equal(out, want)
